@@ -451,6 +451,169 @@ sa_status sa_rows_mse(const void* ref, const void* x, const int32_t* rows, int64
  * buffers, n a multiple of 8 (bf16) or 4 (fp32).  Asynchronous on stream. */
 sa_status sa_l1_error(const void* ref, const void* x, int64_t n, int32_t dtype, double* sums, void* stream);
 
+/* ======================================================================== *
+ * Serving a causal language model: one step over a paged 4-bit cache        *
+ *   sa_cache_plan  -> block tables, slot map, positions, new lengths         *
+ *   sa_rope        -> rotary positions on the new queries and keys           *
+ *   sa_kv4_append  -> the new keys and values into the cache                 *
+ *   sa_kv4_attn    -> attention of the new queries over the cache            *
+ * and sa_window_attn, the token-exact sliding window with first tokens that  *
+ * stay visible ([P4], [P5]) over contiguous K and V, for prefill and for     *
+ * single tokens.                                                             *
+ *                                                                            *
+ * Sequence b has n_k keys and n_q <= any number of query rows; row i sits at  *
+ * position p = n_k - n_q + i.  It sees key j iff                              *
+ *   0 <= j < n_k,  j <= p,  and (window == 0 or p - j < window or j < sinks). *
+ * out = sum_j softmax_j(scale q.k_j) v_j, lse = ln sum_j exp(scale q.k_j); a   *
+ * row that sees no key gets out = 0, lse = -inf.  scale = 0 means 1/sqrt(d).  *
+ * Keys that no row sees may hold anything, infinities and NaN included; a     *
+ * key that some row sees may also be multiplied by a weight of zero in other  *
+ * rows of the call, so a NaN or infinity in its V may reach those.            *
+ * Lengths, tables and slots are read on the device: a value outside its       *
+ * range is brought into it (nothing is read or written out of bounds), the    *
+ * result of that sequence or row is not defined, and the status word          *
+ * (device int32, nullable) gets SA_ERR_INVALID_ARG.                           *
+ * ======================================================================== */
+
+/* q, out [B, Hq, Nq, d], k, v [B, Hkv, Nk, d], lse [B, Hq, Nq], contiguous. */
+typedef struct {
+  int64_t B, Hq, Hkv, Nq, Nk, d;
+  int32_t dtype;
+  int32_t reserved;
+} sa_window_shape;
+
+/* Attention with a sliding window of `window` keys (0 = all earlier keys) and
+ * `sinks` first keys that stay visible, causal, exact to the token.  q_len,
+ * kv_len (device int32 [B], nullable: Nq, Nk) give the rows and keys of a
+ * padded batch's sequences; rows i >= q_len[b] of out and lse are left as they
+ * were.  bf16 with d in {64, 128} runs on the tensor cores; fp32, and other
+ * d up to 256 with d * elem_size a multiple of 16, on the CUDA cores.  All
+ * tensors 16-byte aligned; lse is nullable; out overlaps no input.  ws:
+ * sa_window_attn_workspace() bytes (0 for an invalid shape), 256-byte aligned;
+ * calls that share it must not overlap on the GPU, captured ones included. */
+size_t sa_window_attn_workspace(const sa_window_shape* shape);
+sa_status sa_window_attn(const void* q, const void* k, const void* v, const sa_window_shape* shape,
+                         int64_t window, int64_t sinks, const int32_t* q_len, const int32_t* kv_len,
+                         float scale, void* out, float* lse, int32_t* status, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/* ---- the paged 4-bit cache -----------------------------------------------
+ * uint8 [num_pages][Hkv][page / 16][18 * d], 16-byte aligned; page in {16, 32,
+ * 64, 128}, d in {64, 128}.  Slot s is place s % page of page s / page.  The
+ * d channels of one token's K (and V) of one kv head are cut into groups of
+ * 32; each has a bf16 scale s = bf16(absmax / 7) and 4-bit codes
+ * rint(x / s) in [-7, 7], held as code + 8; a group with an infinity or a NaN
+ * reads back as NaN, a zero group as zeros.  The order of the bytes inside a
+ * 16-token subtile is described in csrc/cache.cu. */
+typedef struct {
+  int64_t num_pages, Hkv;
+  int32_t page, d;
+} sa_kv4_desc;
+
+/* Bytes of the cache, 0 for a bad description. */
+size_t sa_kv4_bytes(const sa_kv4_desc* desc);
+
+/* Row t of k and v (bf16, T tokens of Hkv heads of d contiguous channels;
+ * element strides k_strides, v_strides = {token, head}, multiples of 4;
+ * pointers 8-byte aligned) goes to slot slots[t] (device int32 [T]); -1 =
+ * leave the token out.  The slots of one call must differ: a slot that
+ * appears twice holds a mixture of both tokens afterwards. */
+sa_status sa_kv4_append(const void* k, const void* v, int64_t T, const int64_t k_strides[2],
+                        const int64_t v_strides[2], const int32_t* slots, const sa_kv4_desc* desc, void* cache,
+                        int32_t* status, void* stream);
+
+/* The values of T slots, rounded to bf16: k, v [T, Hkv, d] contiguous,
+ * 16-byte aligned.  Rows of slot -1 are left as they were. */
+sa_status sa_kv4_read(const void* cache, const sa_kv4_desc* desc, const int32_t* slots, int64_t T, void* k,
+                      void* v, int32_t* status, void* stream);
+
+/* Attention over the cache.  q bf16 [T, Hq, d] with element strides q_strides
+ * = {token, head} (multiples of 8, 16-byte aligned), out bf16 [T, Hq, d] and
+ * lse float [T, Hq] (nullable) contiguous.  cu_q (device int32 [B + 1]): the
+ * rows of sequence b are tokens cu_q[b] .. cu_q[b + 1] - 1; tokens past
+ * cu_q[B] are left as they were.  table: device int32 [B][max_blocks], block i
+ * of a sequence holds its keys i * page ..; entries that no visible key needs
+ * may hold anything.  kv_len: device int32 [B], the new tokens included.
+ * window and sinks as above.  ws: sa_kv4_attn_workspace() bytes, 256-byte
+ * aligned, not to be shared by calls that overlap on the GPU. */
+size_t sa_kv4_attn_workspace(const sa_kv4_desc* desc, int64_t Hq);
+sa_status sa_kv4_attn(const void* q, int64_t T, int64_t Hq, const int64_t q_strides[2], const int32_t* cu_q,
+                      int64_t B, const void* cache, const sa_kv4_desc* desc, const int32_t* table,
+                      int64_t max_blocks, const int32_t* kv_len, int64_t window, int64_t sinks, float scale,
+                      void* out, float* lse, int32_t* status, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- rotary positions ------------------------------------------------------
+ * The first rot_dim channels of every head turn in pairs, pair i by p * w_i:
+ *   (y1, y2) = magnitude * (x1 cos - x2 sin, x2 cos + x1 sin),
+ * its channels i and i + rot_dim / 2 (SA_ROPE_HALF) or 2 i and 2 i + 1
+ * (SA_ROPE_INTERLEAVED); the other channels are copied.  inverse = 1 turns
+ * back by the same angle (still times magnitude): the gradient of the forward
+ * rotation.  Angles are exact modulo a turn for every int32 position.
+ * Strides are in elements, {batch, token, head}, channels contiguous; pos is
+ * device int32, token n of batch b at pos[b * pos_stride + n] (0: one row of
+ * positions for all).  k may be NULL (Hk = 0).  q_out may be q and k_out may
+ * be k (in place, equal strides); other overlaps are not allowed, and the
+ * rows of an output must not overlap one another.  d <= 1024. */
+#define SA_ROPE_HALF 0
+#define SA_ROPE_INTERLEAVED 1
+typedef struct {
+  int64_t B, N, Hq, Hk, d;
+  int64_t q_strides[3], q_out_strides[3], k_strides[3], k_out_strides[3];
+  int64_t pos_stride;
+  int32_t rot_dim, layout, dtype, inverse;
+  float magnitude;
+  int32_t reserved;
+} sa_rope_desc;
+sa_status sa_rope(const void* q, void* q_out, const void* k, void* k_out, const int32_t* pos,
+                  const uint64_t* freqs, const sa_rope_desc* desc, void* stream);
+
+/* The frequencies (host uint64 [rot_dim / 2], turns per position in units of
+ * 2^-64; copy them to the device for sa_rope) and the magnitude for
+ *   w_i = base^(-2 i / rot_dim), by scaling:
+ *   NONE    w_i;  LINEAR  w_i / factor;
+ *   NTK     base * factor^(rot_dim / (rot_dim - 2)) in place of base;
+ *   YARN    w_i (1 - r_i) + w_i / factor r_i, r_i a ramp from 0 to 1 between
+ *           the pairs that turn beta_fast and beta_slow times over original_len
+ *           positions (rounded outwards to whole pairs); magnitude
+ *           0.1 ln(factor) + 1.  (1 for the others.) */
+#define SA_ROPE_SCALE_NONE 0
+#define SA_ROPE_SCALE_LINEAR 1
+#define SA_ROPE_SCALE_NTK 2
+#define SA_ROPE_SCALE_YARN 3
+typedef struct {
+  double base, factor;          /* base > 1; factor >= 1 where scaled */
+  double beta_fast, beta_slow;  /* YARN: beta_fast >= beta_slow > 0 */
+  int64_t original_len;         /* YARN: >= 1 */
+  int32_t rot_dim, scaling;     /* rot_dim even, 2 .. 1024 */
+} sa_rope_scaling;
+sa_status sa_rope_frequencies(const sa_rope_scaling* desc, uint64_t* freqs, float* magnitude);
+
+/* ---- block tables and slot maps ---------------------------------------------
+ * One step of a paged cache's bookkeeping.  For request b with kv_len[b]
+ * cached tokens: q_len[b] >= 0 appends that many tokens, -1 ends the request.
+ *   - the pages of ended requests go on top of the stack free_list
+ *     [num_pages] (free_in[0] of its entries are free), in the order of the
+ *     requests and their blocks;
+ *   - then new blocks take pages off its top, in the same order, into table
+ *     [B][max_blocks];
+ *   - free_out[0] = free pages left; new_len[b] = kv_len + q_len (0 for an ended
+ *     request); cu_q [B + 1] = running sum of the tokens; slots, positions
+ *     [max_tokens] = each new token's place in the cache and position, in the
+ *     order of the requests (slot -1, position 0 past the last).
+ * All arrays are device int32; table and free_list are updated in place, no
+ * other output overlaps an input.  Where the step cannot be done (too few
+ * pages, blocks or token places: SA_ERR_CAPACITY; bad lengths: SA_ERR_INVALID_ARG
+ * in status, nullable) nothing changes hands: table and free_list stay, new_len
+ * = kv_len, cu_q = 0, slots = -1, positions = 0, free_out = free_in.
+ * B <= 18000, num_pages * page and max_tokens below 2^31. */
+typedef struct {
+  int64_t B, max_blocks, num_pages, max_tokens;
+  int32_t page, reserved;
+} sa_plan_desc;
+sa_status sa_cache_plan(const int32_t* kv_len, const int32_t* q_len, const sa_plan_desc* desc, int32_t* table,
+                        int32_t* free_list, const int32_t* free_in, int32_t* free_out, int32_t* new_len,
+                        int32_t* cu_q, int32_t* slots, int32_t* positions, int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

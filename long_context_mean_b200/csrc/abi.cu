@@ -27,22 +27,6 @@ sa_status check_launch(const char* what) {
   return SA_OK;
 }
 
-}  // namespace sa
-
-using namespace sa;
-
-namespace {
-
-sa_status check_shape(const sa_shape* s) {
-  if (!s) return set_error(SA_ERR_INVALID_ARG, "shape is NULL");
-  if (s->B <= 0 || s->Hq <= 0 || s->Hkv <= 0 || s->N <= 0 || s->d <= 0 || s->dv <= 0)
-    return set_error(SA_ERR_INVALID_ARG, "shape sizes must be positive");
-  if (s->Hq % s->Hkv != 0) return set_error(SA_ERR_INVALID_ARG, "Hq must be a multiple of Hkv");
-  if (s->dtype != SA_BF16 && s->dtype != SA_FP32) return set_error(SA_ERR_INVALID_ARG, "unknown dtype");
-  if (s->N > (int64_t)INT32_MAX / 2) return set_error(SA_ERR_UNSUPPORTED, "N too large");
-  return SA_OK;
-}
-
 sa_status check_device() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
@@ -57,6 +41,22 @@ bool is_sm100() {
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) return false;
   return major == 10;
+}
+
+}  // namespace sa
+
+using namespace sa;
+
+namespace {
+
+sa_status check_shape(const sa_shape* s) {
+  if (!s) return set_error(SA_ERR_INVALID_ARG, "shape is NULL");
+  if (s->B <= 0 || s->Hq <= 0 || s->Hkv <= 0 || s->N <= 0 || s->d <= 0 || s->dv <= 0)
+    return set_error(SA_ERR_INVALID_ARG, "shape sizes must be positive");
+  if (s->Hq % s->Hkv != 0) return set_error(SA_ERR_INVALID_ARG, "Hq must be a multiple of Hkv");
+  if (s->dtype != SA_BF16 && s->dtype != SA_FP32) return set_error(SA_ERR_INVALID_ARG, "unknown dtype");
+  if (s->N > (int64_t)INT32_MAX / 2) return set_error(SA_ERR_UNSUPPORTED, "N too large");
+  return SA_OK;
 }
 
 int elem_size(int32_t dtype) { return dtype == SA_BF16 ? 2 : 4; }
@@ -215,11 +215,6 @@ sa_status predict_prepare(const char* who, const void* q, const void* k, const s
 bool overlaps(const void* a, const void* b, size_t bytes) {
   const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
   return x < y + bytes && y < x + bytes;
-}
-// [a, a + na) and [b, b + nb) share a byte.
-bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-  return x < y + nb && y < x + na;
 }
 }  // namespace
 

@@ -1,0 +1,804 @@
+// Attention of few query rows over long key ranges (single tokens, short
+// runs of tokens): the 4-bit paged cache (KV4) and contiguous bf16 K, V.
+//
+// Mathematics: for the rows of one kv head (its group of query heads times
+// the sequence's new tokens), o = sum_j 2^(s_j - m) v_j / l with s_j the score in
+// log2 units, m the running maximum and l the running sum; a key range can be
+// cut anywhere and the parts (m, l, o) joined afterwards.
+//
+// Bound by HBM: K and V are read once (KV4: 144 bytes per token and kv head at
+// d = 128), everything else is small.  So:
+//  * the work of the whole batch (every sequence, kv head and row tile times its
+//    16 * SUBS-token tiles) is one line of tiles, cut into equal pieces, one per
+//    CTA, whatever the lengths: a ragged batch and one long sequence fill the
+//    GPU alike.  Lengths are read on the device; a piece may hold several
+//    units (sequence, row tile, kv head) and a unit several pieces.  Units that
+//    lie in one piece are finished there; parts of others go to the workspace
+//    and join_kernel adds them up in a fixed order (no atomics).
+//  * each warp streams its own tiles through its own ring of cp.async stages
+//    (no block barrier in the loop) and multiplies with mma.sync m16n8k16: the
+//    16 side is the tokens (K) or channels (V), the 8 side the query rows, so a
+//    group of 8 rows wastes nothing.  (tcgen05 wants its operands in shared
+//    memory: the widened codes would have to be written there, 4 times the bytes
+//    that arrive.)
+//  * KV4: codes become bf16 integers in registers (one AND-OR puts a nibble
+//    into the mantissa of 128.0, a subtraction of 136 leaves code - 8); K's scales
+//    multiply the 32-channel partial scores in fp32, V's scales multiply P.
+// Rounding: P (and P times the V scale) is rounded to bf16 for the second
+// product; sums, maxima and outputs are fp32.
+#include "sa_internal.cuh"
+
+namespace sa {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kWorkers = 592;      // 148 SMs * 4 CTAs
+constexpr int kMinTiles = 4;       // tiles a piece holds at least: one per warp
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kJoinThreads = 256;
+
+// What a worker leaves for join_kernel.
+struct Piece {
+  int32_t has_head, head_ends;    // its first part belongs to a unit that began in an earlier piece
+  int32_t has_tail;               // its last part begins a unit that a later piece ends
+  int32_t b, row0, kvh, pad0, pad1;   // that unit
+};
+
+struct DecodeArgs {
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;
+  const uint8_t* cache;          // KV4
+  const uint16_t* k;             // bf16, [B][Hkv][Nk][d]
+  const uint16_t* v;
+  const int32_t* table;
+  const int32_t* kv_len;         // nullable (bf16): Nk
+  const int32_t* q_len;          // nullable
+  const int32_t* cu_q;           // nullable
+  int32_t* status;
+  Piece* pieces;
+  float* part_ml;                // [kWorkers][2][rows][2]
+  float* part_o;                 // [kWorkers][2][rows][d]
+  int64_t q_sb, q_st, q_sh;      // element strides of q: sequence, token, head
+  int64_t o_sb, o_st, o_sh;      // of out (lse: the same / d)
+  int64_t T, Nq, Nk;             // packed tokens; tokens and keys per sequence at most
+  int64_t max_blocks, num_pages;
+  int64_t window, sinks;
+  int32_t B, Hkv, group, lg_page;
+  float scale_log2;
+};
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// 16 bytes to shared memory; zeros where !live (nothing is read then).
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
+  const int n = live ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack2bf(float lo, float hi) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t mul2bf(uint32_t a, uint32_t b) {
+  __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+// Nibbles I and I + 4 of w as a bf16 pair of code - 8 (exact).
+template <int I>
+__device__ __forceinline__ uint32_t codes2(uint32_t w) {
+  uint32_t x = ((w >> (4 * I)) & 0x000F000Fu) | 0x43004300u;   // 128 + code
+  __nv_bfloat162 h = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&x), __floats2bfloat162_rn(136.f, 136.f));
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// One unit: a sequence's row tile on one kv head, and the tiles it visits.
+struct Unit {
+  int64_t b, n_k, n_q, q0;         // sequence, its keys and rows' tokens, first packed token
+  int64_t lo, hi, n_sink;          // keys [0, n_sink) and [lo, hi) are visited
+  int32_t row0, kvh;
+};
+
+// Sequence b as the whole batch sees it: tokens, keys, row tiles and tiles.
+template <int TOK, int ROWS>
+__device__ __forceinline__ void sequence(const DecodeArgs& a, int64_t b, Unit& u, int64_t& row_tiles, int64_t& tiles) {
+  u.b = b;
+  if (a.cu_q) {
+    int64_t c0 = a.cu_q[b], c1 = a.cu_q[b + 1];
+    if (c0 < 0 || c1 < c0 || c1 > a.T) {
+      raise_status(a.status, SA_ERR_INVALID_ARG);
+      c0 = max64(0, min64(c0, a.T));
+      c1 = max64(c0, min64(c1, a.T));
+    }
+    u.q0 = c0;
+    u.n_q = c1 - c0;
+  } else {
+    u.q0 = 0;
+    u.n_q = a.q_len ? a.q_len[b] : a.Nq;
+    if (u.n_q < 0 || u.n_q > a.Nq) {
+      raise_status(a.status, SA_ERR_INVALID_ARG);
+      u.n_q = max64(0, min64(u.n_q, a.Nq));
+    }
+  }
+  u.n_k = a.kv_len ? a.kv_len[b] : a.Nk;
+  if (u.n_k < 0 || u.n_k > a.Nk) {
+    raise_status(a.status, SA_ERR_INVALID_ARG);
+    u.n_k = max64(0, min64(u.n_k, a.Nk));
+  }
+  const int64_t first = u.n_k - u.n_q;    // position of the first row
+  u.hi = u.n_k;
+  u.lo = a.window > 0 ? max64(0, first - a.window + 1) : 0;
+  u.lo = min64(u.lo, u.hi);
+  u.n_sink = min64(min64(a.sinks, u.lo), u.hi);
+  // whole tiles; the window's tiles start behind the sinks' tiles
+  const int64_t st = ceil_div_d(u.n_sink, TOK);
+  const int64_t t0 = max64(st, u.lo / TOK);
+  tiles = max64(1, st + max64(0, ceil_div_d(u.hi, TOK) - t0));
+  row_tiles = u.n_q > 0 ? (u.n_q * a.group + ROWS - 1) / ROWS : 0;
+}
+template <int TOK>
+__device__ __forceinline__ int64_t tile_at(const Unit& u, int64_t i) {
+  const int64_t st = ceil_div_d(u.n_sink, TOK);
+  return i < st ? i : max64(st, u.lo / TOK) + (i - st);
+}
+
+// ---------------------------------------------------------------------------
+// Formats: how a tile is fetched and multiplied
+// ---------------------------------------------------------------------------
+// Both give scores s[SUBS][NQ][4] of 16-token subtiles (accumulator layout: rows =
+// tokens lane / 4 and + 8, columns = query rows 2 (lane % 4), + 1) and take P back
+// as B operands.
+template <int D>
+struct Kv4 {
+  static constexpr int G = D / 32, SUBS = 2, TOK = 16 * SUBS, SUB_BYTES = 576 * G, STAGE = SUBS * SUB_BYTES;
+  static constexpr int STAGES = 3, QREGS = 4 * G, TILES = D / 16;
+  static constexpr int CTAS = 4;
+  // Channel of accumulator tile j's row lane / 4 (+ 8 where half).
+  static __device__ __forceinline__ int channel(int j, int half, int r) { return 32 * (j >> 1) + 4 * r + 2 * (j & 1) + half; }
+  static __device__ __forceinline__ void load_q(const uint16_t* p, bool live, int q4, uint32_t* q) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (live) w = *reinterpret_cast<const uint4*>(p + 32 * g + 8 * q4);
+      q[4 * g + 0] = __byte_perm(w.x, w.z, 0x5410);   // channels 0 and 4 of the lane's 8
+      q[4 * g + 1] = __byte_perm(w.x, w.z, 0x7632);
+      q[4 * g + 2] = __byte_perm(w.y, w.w, 0x5410);
+      q[4 * g + 3] = __byte_perm(w.y, w.w, 0x7632);
+    }
+  }
+  int32_t page[SUBS];   // table entries of the tile that is fetched next; kSkip: no row sees the subtile
+  static constexpr int32_t kSkip = INT32_MIN;
+  __device__ __forceinline__ void look(const DecodeArgs& a, const Unit& u, int64_t t0) {
+#pragma unroll
+    for (int s = 0; s < SUBS; ++s) {
+      const int64_t at = t0 + 16 * s;
+      const bool seen = at < u.n_k && (at + 16 > u.lo || at < u.n_sink);
+      page[s] = seen ? max(-1, a.table[u.b * a.max_blocks + (at >> a.lg_page)]) : kSkip;
+    }
+  }
+  // (The stage of a subtile that is left out holds old bytes: their scores are
+  // masked and their scales replaced by zero.)
+  __device__ __forceinline__ void fetch(const DecodeArgs& a, const Unit& u, int64_t t0, uint32_t dst, int lane) {
+#pragma unroll
+    for (int s = 0; s < SUBS; ++s) {
+      if (page[s] == kSkip) continue;
+      const int64_t at = t0 + 16 * s;
+      int64_t pg = page[s];
+      if (pg < 0 || pg >= a.num_pages) {   // the sequence's result is not defined, the access stays inside
+        if (lane == 0) raise_status(a.status, SA_ERR_INVALID_ARG);
+        pg = 0;
+      }
+      const int in = (int)(at & ((1 << a.lg_page) - 1)) >> 4;
+      const uint8_t* src = a.cache + (((pg * a.Hkv + u.kvh) << (a.lg_page - 4)) + in) * (int64_t)SUB_BYTES;
+#pragma unroll
+      for (int i = 0; i < SUB_BYTES / 512; ++i) cp16(dst + s * SUB_BYTES + (i * 32 + lane) * 16, src + (i * 32 + lane) * 16, true);
+      constexpr int rest = SUB_BYTES % 512 / 16;
+      if (rest && lane < rest) {
+        constexpr int o = SUB_BYTES / 512 * 512;
+        cp16(dst + s * SUB_BYTES + o + lane * 16, src + o + lane * 16, true);
+      }
+    }
+  }
+  template <int NQ>
+  static __device__ __forceinline__ void scores(const uint8_t* st, int s, const uint32_t (*q)[QREGS], int lane, float (*out)[4]) {
+    const uint8_t* p = st + s * SUB_BYTES;
+    uint32_t w0[G], w1[G];
+    ld<G>(p + lane * 4 * G, w0);
+    ld<G>(p + 128 * G + lane * 4 * G, w1);
+    uint16_t s0[G], s1[G];
+    ld<G / 2>(p + 512 * G + (lane >> 2) * 2 * G, reinterpret_cast<uint32_t*>(s0));
+    ld<G / 2>(p + 512 * G + ((lane >> 2) + 8) * 2 * G, reinterpret_cast<uint32_t*>(s1));
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[n][e] = 0.f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const uint32_t a0 = codes2<0>(w0[g]), a1 = codes2<0>(w1[g]), a2 = codes2<1>(w0[g]), a3 = codes2<1>(w1[g]);
+      const uint32_t c0 = codes2<2>(w0[g]), c1 = codes2<2>(w1[g]), c2 = codes2<3>(w0[g]), c3 = codes2<3>(w1[g]);
+      const float f0 = bf16_to_f32(s0[g]), f1 = bf16_to_f32(s1[g]);
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        mma16816(c, a0, a1, a2, a3, q[n][4 * g], q[n][4 * g + 1]);
+        mma16816(c, c0, c1, c2, c3, q[n][4 * g + 2], q[n][4 * g + 3]);
+        out[n][0] = fmaf(c[0], f0, out[n][0]);
+        out[n][1] = fmaf(c[1], f0, out[n][1]);
+        out[n][2] = fmaf(c[2], f1, out[n][2]);
+        out[n][3] = fmaf(c[3], f1, out[n][3]);
+      }
+    }
+  }
+  // p: P as B operands (tokens 2 (lane % 4), + 1 and + 8, + 9).  keep: one bit per
+  // token of the subtile whose V counts; a scale of any other token is
+  // whatever the slot holds (possibly NaN) and is replaced by 0.
+  template <int NQ>
+  static __device__ __forceinline__ void accumulate(const uint8_t* st, int s, const uint32_t (*p)[2], uint32_t keep, int lane, float (*o)[TILES][4]) {
+    const uint8_t* b = st + s * SUB_BYTES;
+    uint32_t v0[G], v1[G], s0[G], s1[G];
+    ld<G>(b + 256 * G + lane * 4 * G, v0);
+    ld<G>(b + 384 * G + lane * 4 * G, v1);
+    ld<G>(b + 544 * G + (lane & 3) * 4 * G, s0);
+    ld<G>(b + 560 * G + (lane & 3) * 4 * G, s1);
+    if (keep != 0xFFFFu) {
+      const uint32_t k0 = keep >> (2 * (lane & 3)), k1 = k0 >> 8;
+      const uint32_t m0 = ((k0 & 1) ? 0x0000FFFFu : 0u) | ((k0 & 2) ? 0xFFFF0000u : 0u);
+      const uint32_t m1 = ((k1 & 1) ? 0x0000FFFFu : 0u) | ((k1 & 2) ? 0xFFFF0000u : 0u);
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        s0[g] &= m0;
+        s1[g] &= m1;
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const uint32_t a0 = codes2<0>(v0[g]), a1 = codes2<1>(v0[g]), a2 = codes2<0>(v1[g]), a3 = codes2<1>(v1[g]);
+      const uint32_t c0 = codes2<2>(v0[g]), c1 = codes2<3>(v0[g]), c2 = codes2<2>(v1[g]), c3 = codes2<3>(v1[g]);
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        const uint32_t p0 = mul2bf(p[n][0], s0[g]), p1 = mul2bf(p[n][1], s1[g]);
+        mma16816(o[n][2 * g], a0, a1, a2, a3, p0, p1);
+        mma16816(o[n][2 * g + 1], c0, c1, c2, c3, p0, p1);
+      }
+    }
+  }
+  template <int N>
+  static __device__ __forceinline__ void ld(const uint8_t* p, uint32_t* w) {
+    if constexpr (N == 4) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+    else if constexpr (N == 2) *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+    else *w = *reinterpret_cast<const uint32_t*>(p);
+  }
+};
+
+// Contiguous bf16 K and V.  Rows are swizzled in shared memory so that both
+// operand reads are 16-byte loads without bank conflicts: chunk c (8 channels) of
+// K token t lies at c ^ 4 (t & 1), of V token t at c ^ 2 ((t >> 1) & 3).
+template <int D>
+struct Bf16 {
+  static constexpr int SUBS = 1, TOK = 16, STAGE = TOK * D * 4, STAGES = 3;
+  static constexpr int QREGS = D / 8, TILES = D / 16, CH = D / 8;   // chunks of a row
+  static constexpr int CTAS = 2;
+  static __device__ __forceinline__ int channel(int j, int half, int r) { return D == 128 ? 64 * half + 8 * r + j : 8 * r + 4 * half + j; }
+  static __device__ __forceinline__ void load_q(const uint16_t* p, bool live, int q4, uint32_t* q) {
+#pragma unroll
+    for (int c = 0; c < CH / 4; ++c) {
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (live) w = *reinterpret_cast<const uint4*>(p + (4 * c + q4) * 8);
+      q[4 * c] = w.x;
+      q[4 * c + 1] = w.y;
+      q[4 * c + 2] = w.z;
+      q[4 * c + 3] = w.w;
+    }
+  }
+  __device__ __forceinline__ void look(const DecodeArgs&, const Unit&, int64_t) {}
+  __device__ __forceinline__ void fetch(const DecodeArgs& a, const Unit& u, int64_t t0, uint32_t dst, int lane) {
+    const int64_t base = (u.b * a.Hkv + u.kvh) * a.Nk;
+#pragma unroll
+    for (int i = 0; i < TOK * CH / 32; ++i) {
+      const int e = i * 32 + lane, t = e / CH, c = e % CH;
+      const int64_t key = t0 + t;
+      // keys that no row of the unit sees are not read: they come as zeros
+      const bool live = key < u.n_k && (key >= u.lo || key < u.n_sink);
+      const int64_t at = (base + (live ? key : 0)) * D + c * 8;
+      cp16(dst + t * D * 2 + (c ^ ((t & 1) << 2)) * 16, a.k + at, live);
+      cp16(dst + TOK * D * 2 + t * D * 2 + (c ^ (((t >> 1) & 3) << 1)) * 16, a.v + at, live);
+    }
+  }
+  template <int NQ>
+  static __device__ __forceinline__ void scores(const uint8_t* st, int, const uint32_t (*q)[QREGS], int lane, float (*out)[4]) {
+    const int r = lane >> 2, q4 = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[n][e] = 0.f;
+#pragma unroll
+    for (int c = 0; c < CH / 4; ++c) {
+      const int ch = (4 * c + q4) ^ ((r & 1) << 2);   // rows r and r + 8 have the same parity
+      const uint4 x = *reinterpret_cast<const uint4*>(st + r * D * 2 + ch * 16);
+      const uint4 y = *reinterpret_cast<const uint4*>(st + (r + 8) * D * 2 + ch * 16);
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        mma16816(out[n], x.x, y.x, x.y, y.y, q[n][4 * c], q[n][4 * c + 1]);
+        mma16816(out[n], x.z, y.z, x.w, y.w, q[n][4 * c + 2], q[n][4 * c + 3]);
+      }
+    }
+  }
+  template <int NQ>
+  static __device__ __forceinline__ void accumulate(const uint8_t* st, int, const uint32_t (*p)[2], uint32_t, int lane, float (*o)[TILES][4]) {
+    const int r = lane >> 2, t4 = lane & 3;
+    const uint8_t* b = st + TOK * D * 2;
+    uint4 w[4][D / 64];   // tokens 2 t4, + 1, + 8, + 9
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = 2 * t4 + (i & 1) + 8 * (i >> 1);
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+        w[i][h] = *reinterpret_cast<const uint4*>(b + t * D * 2 + ((r + 8 * h) ^ (((t >> 1) & 3) << 1)) * 16);
+    }
+    auto word = [&](int i, int h, int x) { return reinterpret_cast<const uint32_t*>(&w[i][h])[x]; };
+    // the pair (token, token + 1) of channel x of chunk h
+    auto pair = [&](int i, int h, int x) {
+      return __byte_perm(word(i, h, x >> 1), word(i + 1, h, x >> 1), (x & 1) ? 0x7632 : 0x5410);
+    };
+#pragma unroll
+    for (int j = 0; j < TILES; ++j) {
+      const int h1 = D == 128 ? 1 : 0, x1 = D == 128 ? j : 4 + j;
+      const uint32_t a0 = pair(0, 0, j), a1 = pair(0, h1, x1), a2 = pair(2, 0, j), a3 = pair(2, h1, x1);
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) mma16816(o[n][j], a0, a1, a2, a3, p[n][0], p[n][1]);
+    }
+  }
+};
+
+// Row R of the sequence's n_q * group rows on kv head kvh: its token and query head.
+__device__ __forceinline__ int64_t row_off(const DecodeArgs& a, const Unit& u, int64_t R, int64_t sb, int64_t st, int64_t sh) {
+  const int64_t i = R / a.group, h = (int64_t)u.kvh * a.group + R % a.group;
+  return (a.cu_q ? (u.q0 + i) * st : u.b * sb + i * st) + h * sh;
+}
+
+// o (unnormalised, relative to m) of 8 channels of row R, to its place.
+template <int D>
+__device__ __forceinline__ void finish_row(const DecodeArgs& a, const Unit& u, int64_t R, int c8, float m, float l, const float* o) {
+  const int64_t off = row_off(a, u, R, a.o_sb, a.o_st, a.o_sh);
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // no visible key: zeros; NaN stays
+  uint4 w;
+  uint32_t* p = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = pack2bf(o[2 * i] * inv, o[2 * i + 1] * inv);
+  *reinterpret_cast<uint4*>(a.out + off + c8 * 8) = w;
+  if (c8 == 0 && a.lse) a.lse[off / D] = (m + log2f(l)) * kLn2;   // log2f(0) = -inf
+}
+
+template <class F, int D, int NQ>
+__global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel(const __grid_constant__ DecodeArgs a) {
+  constexpr int ROWS = 8 * NQ, TOK = F::TOK;
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ int64_t scan[kWarps];
+  __shared__ int64_t found_b, found_off;
+  __shared__ float wm[kWarps][ROWS], wl[kWarps][ROWS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = lane >> 2, t4 = lane & 3;
+
+  // Where this piece of the line of tiles starts.
+  const int64_t per_thread = (a.B + kThreads - 1) / kThreads;
+  const int64_t b0 = min64(a.B, tid * per_thread), b1 = min64(a.B, b0 + per_thread);
+  int64_t sum = 0;
+  for (int64_t b = b0; b < b1; ++b) {
+    Unit u;
+    int64_t rt, tl;
+    sequence<TOK, ROWS>(a, b, u, rt, tl);
+    sum += rt * a.Hkv * tl;
+  }
+  int64_t inc = sum;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) scan[warp] = inc;
+  if (tid == 0) found_b = -1;
+  __syncthreads();
+  int64_t before = 0, W = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += scan[w];
+    W += scan[w];
+  }
+  const int64_t per = max64(kMinTiles, (W + gridDim.x - 1) / gridDim.x);
+  const int64_t start = min64(W, blockIdx.x * per), end = min64(W, start + per);
+  int64_t pos = before + inc - sum;
+  if (start < end && start >= pos && start < pos + sum) {
+    for (int64_t b = b0; b < b1; ++b) {
+      Unit u;
+      int64_t rt, tl;
+      sequence<TOK, ROWS>(a, b, u, rt, tl);
+      const int64_t n = rt * a.Hkv * tl;
+      if (start < pos + n) {
+        found_b = b;
+        found_off = start - pos;
+        break;
+      }
+      pos += n;
+    }
+  }
+  __syncthreads();
+  Piece piece{};
+  int64_t b = found_b, off = found_off;
+
+  F f;
+  const uint32_t ring = smem_addr(sm) + warp * (F::STAGES * F::STAGE);
+  const uint8_t* ring_p = sm + warp * (F::STAGES * F::STAGE);
+  int64_t at = start;
+  while (at < end && b < a.B) {
+    Unit u;
+    int64_t rt, tl;
+    sequence<TOK, ROWS>(a, b, u, rt, tl);
+    const int64_t whole = rt * a.Hkv * tl;
+    if (off >= whole) {   // next sequence
+      off -= whole;
+      ++b;
+      continue;
+    }
+    const int64_t unit = off / tl, i0 = off - unit * tl;
+    u.kvh = (int32_t)(unit % a.Hkv);
+    u.row0 = (int32_t)(unit / a.Hkv) * ROWS;
+    const int64_t i1 = min64(tl, i0 + (end - at));
+    const int64_t rows_all = u.n_q * a.group;
+
+    uint32_t q[NQ][F::QREGS];
+    int64_t qpos[NQ][2];   // positions of this lane's columns (query rows)
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const int64_t R = u.row0 + 8 * n + r;
+      const bool live = R < rows_all;
+      F::load_q(a.q + row_off(a, u, live ? R : 0, a.q_sb, a.q_st, a.q_sh), live, t4, q[n]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) qpos[n][c] = u.n_k - u.n_q + min64(rows_all - 1, u.row0 + 8 * n + 2 * t4 + c) / a.group;
+    }
+    const int64_t p_min = u.n_k - u.n_q + u.row0 / a.group;
+    const int64_t p_max = u.n_k - u.n_q + min64(rows_all - 1, u.row0 + ROWS - 1) / a.group;
+
+    float o[NQ][F::TILES][4], m[NQ][2], l[NQ][2];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+      for (int j = 0; j < F::TILES; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][j][e] = 0.f;
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+    }
+
+    const int64_t first = i0 + warp;
+    const int64_t mine = first < i1 ? (i1 - first + kWarps - 1) / kWarps : 0;
+    if (mine > 0) f.look(a, u, tile_at<TOK>(u, first) * TOK);
+    int64_t sent = 0;
+    auto send = [&]() {
+      if (sent < mine) {
+        f.fetch(a, u, tile_at<TOK>(u, first + sent * kWarps) * TOK, ring + (uint32_t)(sent % F::STAGES) * F::STAGE, lane);
+        ++sent;
+        if (sent < mine) f.look(a, u, tile_at<TOK>(u, first + sent * kWarps) * TOK);
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < F::STAGES - 1; ++s) send();
+    for (int64_t i = 0; i < mine; ++i) {
+      cp_wait<F::STAGES - 2>();
+      __syncwarp();
+      send();
+      const uint8_t* st = ring_p + (i % F::STAGES) * F::STAGE;
+      const int64_t t0 = tile_at<TOK>(u, first + i * kWarps) * TOK;
+      float s[F::SUBS][NQ][4];
+#pragma unroll
+      for (int x = 0; x < F::SUBS; ++x) F::template scores<NQ>(st, x, q, lane, s[x]);
+      const bool all = t0 + TOK - 1 <= p_min && t0 + TOK <= u.n_k &&
+                       (a.window == 0 || p_max - t0 < a.window || t0 + TOK <= a.sinks);
+      uint32_t keep[F::SUBS];
+#pragma unroll
+      for (int x = 0; x < F::SUBS; ++x) keep[x] = 0xFFFFu;
+#pragma unroll
+      for (int x = 0; x < F::SUBS; ++x)
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[x][n][e] *= a.scale_log2;
+      if (!all) {
+#pragma unroll
+        for (int x = 0; x < F::SUBS; ++x) {
+#pragma unroll
+          for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int64_t key = t0 + 16 * x + r + 8 * (e >> 1), p = qpos[n][e & 1];
+              const bool see = key < u.n_k && key <= p && (a.window == 0 || p - key < a.window || key < a.sinks);
+              if (!see) s[x][n][e] = -INFINITY;
+            }
+          // tokens that some row of the unit may see
+          const int64_t k0 = t0 + 16 * x + (lane & 15);
+          keep[x] = __ballot_sync(0xffffffffu, k0 < u.n_k && (k0 >= u.lo || k0 < u.n_sink)) & 0xFFFFu;
+        }
+      }
+      bool moved = false;
+      float corr[NQ][2], ref[NQ][2];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float x = fmaxf(s[0][n][c], s[0][n][c + 2]);
+#pragma unroll
+          for (int y = 1; y < F::SUBS; ++y) x = fmaxf(x, fmaxf(s[y][n][c], s[y][n][c + 2]));
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+          const float mn = fmaxf(m[n][c], x);
+          ref[n][c] = mn == -INFINITY ? 0.f : mn;
+          corr[n][c] = ex2f(m[n][c] - ref[n][c]);
+          moved |= mn != m[n][c];
+          m[n][c] = mn;
+        }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          l[n][0] *= corr[n][0];
+          l[n][1] *= corr[n][1];
+#pragma unroll
+          for (int j = 0; j < F::TILES; ++j) {
+            o[n][j][0] *= corr[n][0];
+            o[n][j][1] *= corr[n][1];
+            o[n][j][2] *= corr[n][0];
+            o[n][j][3] *= corr[n][1];
+          }
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < F::SUBS; ++x) {
+        uint32_t p[NQ][2];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          float e[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) e[y] = ex2f(s[x][n][y] - ref[n][y & 1]);
+          l[n][0] += e[0] + e[2];
+          l[n][1] += e[1] + e[3];
+          p[n][0] = transpose8(pack2bf(e[0], e[1]));
+          p[n][1] = transpose8(pack2bf(e[2], e[3]));
+        }
+        F::template accumulate<NQ>(st, x, p, keep[x], lane, o);
+      }
+    }
+    cp_wait<0>();
+
+    // Join the four warps' parts in shared memory (over the rings).
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], d);
+        if (r == 0) {
+          wm[warp][8 * n + 2 * t4 + c] = m[n][c];
+          wl[warp][8 * n + 2 * t4 + c] = l[n][c];
+        }
+      }
+    __syncthreads();
+    float* os = reinterpret_cast<float*>(sm);   // [warp][ROWS][D + 4]
+    constexpr int OS = D + 4;
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int j = 0; j < F::TILES; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          os[(warp * ROWS + 8 * n + 2 * t4 + (e & 1)) * OS + F::channel(j, e >> 1, r)] = o[n][j][e];
+    __syncthreads();
+    const bool begins = i0 == 0, ends = i1 == tl;
+    const int64_t slot = (int64_t)blockIdx.x * 2 + (begins ? 1 : 0);
+    for (int e = tid; e < ROWS * (D / 8); e += kThreads) {
+      const int row = e / (D / 8), c8 = e % (D / 8);
+      float mx = wm[0][row];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) mx = fmaxf(mx, wm[w][row]);
+      const float rf = mx == -INFINITY ? 0.f : mx;
+      float acc[8] = {}, ls = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float g = ex2f(wm[w][row] - rf);
+        ls += g * wl[w][row];
+        const float* src = os + (w * ROWS + row) * OS + c8 * 8;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) acc[x] += g * src[x];
+      }
+      const int64_t R = u.row0 + row;
+      if (R >= rows_all) continue;
+      if (begins && ends) {
+        finish_row<D>(a, u, R, c8, mx, ls, acc);
+      } else {
+        float* dst = a.part_o + (slot * ROWS + row) * D + c8 * 8;
+        *reinterpret_cast<float4*>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        *reinterpret_cast<float4*>(dst + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        if (c8 == 0) *reinterpret_cast<float2*>(a.part_ml + (slot * ROWS + row) * 2) = make_float2(mx, ls);
+      }
+    }
+    if (!begins) {
+      piece.has_head = 1;
+      piece.head_ends = ends;
+    } else if (!ends) {
+      piece.has_tail = 1;
+      piece.b = (int32_t)u.b;
+      piece.row0 = u.row0;
+      piece.kvh = u.kvh;
+    }
+    at += i1 - i0;
+    off += i1 - i0;
+    __syncthreads();
+  }
+  if (tid == 0) a.pieces[blockIdx.x] = piece;
+}
+
+// Adds up the parts of the unit that begins in piece blockIdx.x and ends in a
+// later one, in the order of the pieces.  Launched as a dependent of
+// decode_kernel: it waits for that grid's writes.
+template <class F, int D, int NQ>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ DecodeArgs a, int pieces) {
+  constexpr int ROWS = 8 * NQ;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Piece p = a.pieces[blockIdx.x];
+  if (!p.has_tail) return;
+  int last = blockIdx.x;   // the piece that ends the unit
+  while (last + 1 < pieces) {
+    ++last;
+    if (a.pieces[last].head_ends) break;
+  }
+  Unit u;
+  int64_t rt, tl;
+  sequence<F::TOK, ROWS>(a, p.b, u, rt, tl);
+  u.row0 = p.row0;
+  u.kvh = p.kvh;
+  const int64_t rows_all = u.n_q * a.group;
+  for (int e = threadIdx.x; e < ROWS * (D / 8); e += kJoinThreads) {
+    const int row = e / (D / 8), c8 = e % (D / 8);
+    if (u.row0 + row >= rows_all) continue;
+    float m = -INFINITY, l = 0.f, acc[8] = {};
+    for (int w = blockIdx.x; w <= last; ++w) {
+      const int64_t slot = (int64_t)w * 2 + (w == (int)blockIdx.x ? 1 : 0);
+      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (slot * ROWS + row) * 2);
+      const float* src = a.part_o + (slot * ROWS + row) * D + c8 * 8;
+      const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + 4);
+      const float mn = fmaxf(m, ml.x), rf = mn == -INFINITY ? 0.f : mn;
+      const float g = ex2f(m - rf), h = ex2f(ml.x - rf);
+      l = l * g + ml.y * h;
+      const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = acc[i] * g + v[i] * h;
+      m = mn;
+    }
+    finish_row<D>(a, u, u.row0 + row, c8, m, l, acc);
+  }
+}
+
+size_t ws_bytes(int64_t rows, int64_t d) {
+  return align_up(kWorkers * sizeof(Piece), 256) + align_up((size_t)kWorkers * 2 * rows * 2 * sizeof(float), 256) +
+         (size_t)kWorkers * 2 * rows * d * sizeof(float);
+}
+
+template <class F, int D, int NQ>
+sa_status launch(DecodeArgs& a, int64_t max_tiles, void* ws, cudaStream_t st) {
+  constexpr int ROWS = 8 * NQ;
+  constexpr int smem_ring = kWarps * F::STAGES * F::STAGE, smem_join = kWarps * ROWS * (D + 4) * 4;
+  constexpr int smem = smem_ring > smem_join ? smem_ring : smem_join;
+  char* w = static_cast<char*>(ws);
+  a.pieces = reinterpret_cast<Piece*>(w);
+  w += align_up(kWorkers * sizeof(Piece), 256);
+  a.part_ml = reinterpret_cast<float*>(w);
+  w += align_up((size_t)kWorkers * 2 * ROWS * 2 * sizeof(float), 256);
+  a.part_o = reinterpret_cast<float*>(w);
+  if (cudaFuncSetAttribute(decode_kernel<F, D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return set_error(SA_ERR_CUDA, "cudaFuncSetAttribute(decode_kernel) failed");
+  const int workers = NQ == 1 ? 148 * F::CTAS : 148 * 2;
+  const int grid = (int)max64(1, min64(workers, ceil_div(max_tiles, kMinTiles)));
+  decode_kernel<F, D, NQ><<<grid, kThreads, smem, st>>>(a);
+  if (sa_status e = check_launch("decode_kernel")) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, join_kernel<F, D, NQ>, a, grid) != cudaSuccess)
+    return check_launch("join_kernel");
+  return SA_OK;
+}
+
+template <template <int> class F>
+sa_status launch_format(DecodeArgs& a, int64_t d, int nq, int64_t max_tiles, void* ws, cudaStream_t st) {
+  if (d == 128)
+    return nq == 1 ? launch<F<128>, 128, 1>(a, max_tiles, ws, st) : launch<F<128>, 128, 2>(a, max_tiles, ws, st);
+  return nq == 1 ? launch<F<64>, 64, 1>(a, max_tiles, ws, st) : launch<F<64>, 64, 2>(a, max_tiles, ws, st);
+}
+
+}  // namespace
+
+size_t decode_ws_bytes(int64_t d) { return ws_bytes(16, d); }
+
+sa_status launch_kv4_attn(const Kv4AttnArgs& x, cudaStream_t st) {
+  DecodeArgs a{};
+  a.q = static_cast<const uint16_t*>(x.q);
+  a.out = static_cast<uint16_t*>(x.out);
+  a.lse = x.lse;
+  a.cache = static_cast<const uint8_t*>(x.cache);
+  a.table = x.table;
+  a.kv_len = x.kv_len;
+  a.cu_q = x.cu_q;
+  a.status = x.status;
+  a.q_sb = a.q_st = x.q_strides[0];
+  a.q_sh = x.q_strides[1];
+  a.o_sb = a.o_st = x.Hq * x.desc.d;
+  a.o_sh = x.desc.d;
+  a.T = x.T;
+  a.Nq = 1;
+  a.Nk = x.max_blocks * x.desc.page;
+  a.max_blocks = x.max_blocks;
+  a.num_pages = x.desc.num_pages;
+  a.window = x.window;
+  a.sinks = x.sinks;
+  a.B = (int32_t)x.B;
+  a.Hkv = (int32_t)x.desc.Hkv;
+  a.group = (int32_t)(x.Hq / x.desc.Hkv);
+  while ((1LL << a.lg_page) < x.desc.page) ++a.lg_page;
+  a.scale_log2 = x.scale * kLog2e;
+  // Two column tiles (16 rows) a unit where the average sequence has more than 8 rows.
+  const int nq = x.T * a.group > 8 * x.B ? 2 : 1;
+  const int64_t row_tiles = ceil_div(x.T * a.group, 8 * nq) + x.B;
+  const int64_t max_tiles = row_tiles * a.Hkv * ceil_div(a.Nk, Kv4<128>::TOK);
+  return launch_format<Kv4>(a, x.desc.d, nq, max_tiles, x.ws, st);
+}
+
+sa_status launch_window_decode(const WindowArgs& x, cudaStream_t st) {
+  DecodeArgs a{};
+  a.q = static_cast<const uint16_t*>(x.q);
+  a.k = static_cast<const uint16_t*>(x.k);
+  a.v = static_cast<const uint16_t*>(x.v);
+  a.out = static_cast<uint16_t*>(x.out);
+  a.lse = x.lse;
+  a.kv_len = x.kv_len;
+  a.q_len = x.q_len;
+  a.status = x.status;
+  const sa_window_shape& s = x.shape;
+  a.q_st = a.o_st = s.d;
+  a.q_sh = a.o_sh = s.Nq * s.d;
+  a.q_sb = a.o_sb = s.Hq * s.Nq * s.d;
+  a.Nq = s.Nq;
+  a.Nk = s.Nk;
+  a.window = x.window;
+  a.sinks = x.sinks;
+  a.B = (int32_t)s.B;
+  a.Hkv = (int32_t)s.Hkv;
+  a.group = (int32_t)(s.Hq / s.Hkv);
+  a.scale_log2 = x.scale * kLog2e;
+  const int nq = s.Nq * a.group > 8 ? 2 : 1;
+  int64_t keys = s.Nk;
+  if (x.window > 0) keys = min64(keys, x.window + x.sinks + s.Nq + 2 * Bf16<128>::TOK);
+  const int64_t max_tiles = s.B * ceil_div(s.Nq * a.group, 8 * nq) * a.Hkv * ceil_div(keys, Bf16<128>::TOK);
+  return launch_format<Bf16>(a, s.d, nq, max_tiles, x.ws, st);
+}
+
+}  // namespace sa

@@ -16,6 +16,13 @@ namespace sa {
 // ---------------------------------------------------------------------------
 sa_status set_error(sa_status code, const char* fmt, ...);
 sa_status check_launch(const char* what);
+sa_status check_device();   // SA_ERR_CUDA without a usable device
+bool is_sm100();            // the current device is a B200 (compute capability 10.x)
+// [a, a + na) and [b, b + nb) share a byte.
+inline bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y + nb && y < x + na;
+}
 
 // ---------------------------------------------------------------------------
 // Device helpers
@@ -88,6 +95,7 @@ __device__ __forceinline__ void unpack16(const uint4& u, float, float* f) {
 __host__ __device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
 __host__ __device__ __forceinline__ int64_t max64(int64_t a, int64_t b) { return a > b ? a : b; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+__device__ __forceinline__ int64_t ceil_div_d(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline size_t align_up(size_t a, size_t b) { return (a + b - 1) / b * b; }
 
 // ---------------------------------------------------------------------------
@@ -178,5 +186,50 @@ sa_status launch_tile_scales(const sa_mask& m, int64_t B, int64_t Hq, int64_t Hk
 sa_status launch_l1(const void* ref, const void* x, int64_t n, int32_t dtype, double* sums, cudaStream_t st);
 sa_status launch_attn_tc(const AttnArgs& a, cudaStream_t st);
 bool attn_tc_supported(const sa_shape& s, int bq, int bk);
+
+// Serving operators (arguments validated in serve_abi.cu).
+struct WindowArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  float* lse;
+  const int32_t* q_len;    // nullable
+  const int32_t* kv_len;   // nullable
+  int32_t* status;
+  sa_window_shape shape;
+  int64_t window, sinks;
+  float scale;
+  void* ws;
+};
+struct Kv4AttnArgs {
+  const void* q;
+  const void* cache;
+  const int32_t* cu_q;
+  const int32_t* table;
+  const int32_t* kv_len;
+  void* out;
+  float* lse;
+  int32_t* status;
+  sa_kv4_desc desc;
+  int64_t T, Hq, B, max_blocks;
+  int64_t q_strides[2];
+  int64_t window, sinks;
+  float scale;
+  void* ws;
+};
+size_t decode_ws_bytes(int64_t d);
+sa_status launch_window_decode(const WindowArgs& a, cudaStream_t st);   // bf16, d in {64, 128}
+sa_status launch_window_simt(const WindowArgs& a, cudaStream_t st);     // any dtype and d
+sa_status launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t st);
+sa_status launch_kv4_append(const void* k, const void* v, int64_t T, const int64_t* ks, const int64_t* vs,
+                            const int32_t* slots, const sa_kv4_desc& d, void* cache, int32_t* status, cudaStream_t st);
+sa_status launch_kv4_read(const void* cache, const sa_kv4_desc& d, const int32_t* slots, int64_t T, void* k, void* v,
+                          int32_t* status, cudaStream_t st);
+sa_status launch_plan(const int32_t* kv_len, const int32_t* q_len, const sa_plan_desc& d, int32_t* table,
+                      int32_t* free_list, const int32_t* free_in, int32_t* free_out, int32_t* new_len, int32_t* cu_q,
+                      int32_t* slots, int32_t* positions, int32_t* status, cudaStream_t st);
+sa_status launch_rope(const void* q, void* q_out, const void* k, void* k_out, const int32_t* pos,
+                      const uint64_t* freqs, const sa_rope_desc& d, cudaStream_t st);
 
 }  // namespace sa

@@ -38,7 +38,9 @@ EXPORTS = ["sa_version", "sa_last_error", "sa_attn_kernel_path", "sa_attn_worksp
            "sa_mask_from_blocks", "sa_block_sparse_attn", "sa_dense_attn", "sa_read_status", "sa_l1_error",
            "sa_head_placement", "sa_reorder_heads", "sa_rows_attn", "sa_rows_mse",
            "sa_quantize_blocks", "sa_attn_qk8_workspace", "sa_block_sparse_attn_qk8",
-           "sa_reorder_predict_mask_q8", "sa_forward_host_workspace", "sa_forward_host"]
+           "sa_reorder_predict_mask_q8", "sa_forward_host_workspace", "sa_forward_host",
+           "sa_window_attn_workspace", "sa_window_attn", "sa_kv4_bytes", "sa_kv4_append", "sa_kv4_read",
+           "sa_kv4_attn_workspace", "sa_kv4_attn", "sa_rope_frequencies", "sa_rope", "sa_cache_plan"]
 
 
 class SAError(RuntimeError):
@@ -74,6 +76,37 @@ class Mask(ctypes.Structure):
                 ("col_capacity", ctypes.c_int64), ("nqb", ctypes.c_int64), ("nkb", ctypes.c_int64),
                 ("bq", ctypes.c_int32), ("bk", ctypes.c_int32), ("causal", ctypes.c_int32),
                 ("reserved", ctypes.c_int32)]
+
+
+class WindowShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("Hq", ctypes.c_int64), ("Hkv", ctypes.c_int64), ("Nq", ctypes.c_int64),
+                ("Nk", ctypes.c_int64), ("d", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class KV4Desc(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int64), ("Hkv", ctypes.c_int64), ("page", ctypes.c_int32),
+                ("d", ctypes.c_int32)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("N", ctypes.c_int64), ("Hq", ctypes.c_int64), ("Hk", ctypes.c_int64),
+                ("d", ctypes.c_int64), ("q_strides", ctypes.c_int64 * 3), ("q_out_strides", ctypes.c_int64 * 3),
+                ("k_strides", ctypes.c_int64 * 3), ("k_out_strides", ctypes.c_int64 * 3),
+                ("pos_stride", ctypes.c_int64), ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("inverse", ctypes.c_int32), ("magnitude", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+class RopeScaling(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_double), ("factor", ctypes.c_double), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double), ("original_len", ctypes.c_int64), ("rot_dim", ctypes.c_int32),
+                ("scaling", ctypes.c_int32)]
+
+
+class PlanDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("max_blocks", ctypes.c_int64), ("num_pages", ctypes.c_int64),
+                ("max_tokens", ctypes.c_int64), ("page", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -130,6 +163,18 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                            ctypes.POINTER(MaskParams), I32]),
         "sa_forward_host": (I32, [P, P, P, P, P, ctypes.POINTER(Shape), ctypes.POINTER(LayoutDesc),
                                   ctypes.POINTER(MaskParams), F, F, I32, P, SZ, P, ctypes.POINTER(P * 3)]),
+        "sa_window_attn_workspace": (SZ, [ctypes.POINTER(WindowShape)]),
+        "sa_window_attn": (I32, [P, P, P, ctypes.POINTER(WindowShape), I64, I64, P, P, F, P, P, P, P, SZ, P]),
+        "sa_kv4_bytes": (SZ, [ctypes.POINTER(KV4Desc)]),
+        "sa_kv4_append": (I32, [P, P, I64, ctypes.POINTER(I64 * 2), ctypes.POINTER(I64 * 2), P,
+                                ctypes.POINTER(KV4Desc), P, P, P]),
+        "sa_kv4_read": (I32, [P, ctypes.POINTER(KV4Desc), P, I64, P, P, P, P]),
+        "sa_kv4_attn_workspace": (SZ, [ctypes.POINTER(KV4Desc), I64]),
+        "sa_kv4_attn": (I32, [P, I64, I64, ctypes.POINTER(I64 * 2), P, I64, P, ctypes.POINTER(KV4Desc), P, I64, P,
+                              I64, I64, F, P, P, P, P, SZ, P]),
+        "sa_rope_frequencies": (I32, [ctypes.POINTER(RopeScaling), P, ctypes.POINTER(F)]),
+        "sa_rope": (I32, [P, P, P, P, P, P, ctypes.POINTER(RopeDesc), P]),
+        "sa_cache_plan": (I32, [P, P, ctypes.POINTER(PlanDesc), P, P, P, P, P, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -382,6 +427,254 @@ def rows_mse(ref, x, rows, out, status=None, stream=None):
 def read_status(status, stream=None) -> int:
     """Synchronises the stream and returns the device status code (no raise)."""
     return int(load().sa_read_status(_ptr(status), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Serving a causal model: cache plan, rotary positions, 4-bit paged cache,
+# window attention
+# ---------------------------------------------------------------------------
+# These take tensors of any one device (which need not be the current one)
+# and run on `stream`, or on that device's current stream.
+
+def _need(ok, msg):
+    if not ok:
+        raise ValueError(msg)
+
+
+def _same(t, dtype, shape, name, device, contiguous=True):
+    """t is a CUDA tensor of this dtype, shape (None entries: any) and device."""
+    import torch
+    _need(isinstance(t, torch.Tensor) and t.dtype == dtype, f"{name} must be a {dtype} tensor")
+    _need(t.device == device and t.is_cuda, f"{name} must be on the same CUDA device as the other tensors")
+    _need(t.dim() == len(shape) and all(w is None or n == w for n, w in zip(t.shape, shape)),
+          f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    _need(not contiguous or t.is_contiguous(), f"{name} must be contiguous")
+
+
+def _index(t, n, name, device):
+    """An int32 [n] argument, or None."""
+    import torch
+    if t is not None:
+        _same(t, torch.int32, (n,), name, device)
+    return _ptr(t)
+
+
+def _on(device, stream, fn, *args):
+    """fn(*args, stream) with `device` current."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(stream)))
+
+
+def _ws_args(ws):
+    import torch
+    _need(isinstance(ws, torch.Tensor) and ws.is_contiguous(), "ws must be a contiguous tensor")
+    return _ptr(ws), ws.numel() * ws.element_size()
+
+
+def make_window_shape(q, k) -> WindowShape:
+    B, Hq, Nq, d = q.shape
+    return WindowShape(B, Hq, k.shape[1], Nq, k.shape[2], d, dtype_code(q), 0)
+
+
+def window_attn_workspace(q, k, v) -> int:
+    """Bytes of the workspace that window_attn needs for tensors of these shapes."""
+    return int(load().sa_window_attn_workspace(ctypes.byref(make_window_shape(q, k))))
+
+
+def window_attn(q, k, v, out, lse=None, *, window=0, sinks=0, q_len=None, kv_len=None, scale=0.0, status=None,
+                ws=None, stream=None):
+    """Causal attention in which a query sees the last `window` keys (0: all)
+    and the first `sinks` ones: q, out [B, Hq, Nq, d], k, v [B, Hkv, Nk, d], lse
+    [B, Hq, Nq] float32.  Row i of a sequence with n_q rows and n_k keys
+    sits at position n_k - n_q + i; q_len, kv_len (int32 [B]) are the lengths
+    of a padded batch, and rows past q_len stay as they were.  ws: a
+    workspace() of window_attn_workspace() bytes (allocated per call if None)."""
+    import torch
+    dev = q.device
+    _need(q.dim() == 4 and k.dim() == 4, "q and k must have four axes")
+    B, Hq, Nq, d = q.shape
+    _same(q, q.dtype, (B, Hq, Nq, d), "q", dev)
+    _same(k, q.dtype, (B, None, None, d), "k", dev)
+    _same(v, q.dtype, tuple(k.shape), "v", dev)
+    _same(out, q.dtype, tuple(q.shape), "out", dev)
+    if lse is not None:
+        _same(lse, torch.float32, (B, Hq, Nq), "lse", dev)
+    shape = make_window_shape(q, k)
+    if ws is None:
+        ws = workspace(load().sa_window_attn_workspace(ctypes.byref(shape)), dev)
+    _on(dev, stream, load().sa_window_attn, _ptr(q), _ptr(k), _ptr(v), ctypes.byref(shape), int(window), int(sinks),
+        _index(q_len, B, "q_len", dev), _index(kv_len, B, "kv_len", dev), float(scale), _ptr(out), _ptr(lse),
+        _index(status, 1, "status", dev), *_ws_args(ws))
+
+
+class KV4Cache:
+    """A paged 4-bit cache: pages uint8 [num_pages, Hkv, page / 16, 18 d]
+    (``KV4Cache.allocate`` makes them) and their description."""
+
+    def __init__(self, pages, page: int, d: int):
+        import torch
+        _need(pages.dim() == 4, "the pages must have four axes")
+        _same(pages, torch.uint8, (None, None, page // 16, 18 * d), "pages", pages.device)
+        self.pages, self.page, self.d = pages, int(page), int(d)
+        self.num_pages, self.Hkv = pages.shape[:2]
+        self.desc = KV4Desc(self.num_pages, self.Hkv, self.page, self.d)
+        _need(load().sa_kv4_bytes(ctypes.byref(self.desc)) == pages.numel(),
+              "page must be 16, 32, 64 or 128, d 64 or 128, and the cache must not be empty")
+
+    @classmethod
+    def allocate(cls, num_pages, Hkv, page, d, device="cuda"):
+        import torch
+        return cls(torch.zeros(num_pages, Hkv, page // 16, 18 * d, dtype=torch.uint8, device=device), page, d)
+
+
+_I64x2, _I64x3 = ctypes.c_int64 * 2, ctypes.c_int64 * 3
+
+
+def _rows_of(t, name, T, H, d, dev):
+    import torch
+    _same(t, torch.bfloat16, (T, H, d), name, dev, contiguous=False)
+    _need(d == 1 or t.stride(2) == 1, f"the channels of {name} must be contiguous")
+    return ctypes.byref(_I64x2(t.stride(0), t.stride(1)))
+
+
+def kv4_append(k, v, slots, cache: KV4Cache, *, status=None, stream=None):
+    """Tokens k, v (bf16 [T, Hkv, d]) into the slots of the cache (int32 [T],
+    -1 = leave out; the others must differ)."""
+    T, dev = k.shape[0], cache.pages.device
+    ks, vs = (_rows_of(t, n, T, cache.Hkv, cache.d, dev) for t, n in ((k, "k"), (v, "v")))
+    _on(dev, stream, load().sa_kv4_append, _ptr(k), _ptr(v), T, ks, vs, _index(slots, T, "slots", dev),
+        ctypes.byref(cache.desc), _ptr(cache.pages), _index(status, 1, "status", dev))
+
+
+def kv4_read(cache: KV4Cache, slots, k, v, *, status=None, stream=None):
+    """The values of the cache's slots (int32 [T]) into k, v (bf16 [T, Hkv, d])."""
+    import torch
+    T, dev = k.shape[0], cache.pages.device
+    _same(k, torch.bfloat16, (T, cache.Hkv, cache.d), "k", dev)
+    _same(v, torch.bfloat16, (T, cache.Hkv, cache.d), "v", dev)
+    _on(dev, stream, load().sa_kv4_read, _ptr(cache.pages), ctypes.byref(cache.desc), _index(slots, T, "slots", dev), T,
+        _ptr(k), _ptr(v), _index(status, 1, "status", dev))
+
+
+def kv4_attn_workspace(cache: KV4Cache, Hq: int) -> int:
+    """Bytes of the workspace that kv4_attn needs."""
+    return int(load().sa_kv4_attn_workspace(ctypes.byref(cache.desc), int(Hq)))
+
+
+def kv4_attn(q, cache: KV4Cache, table, kv_len, out, lse=None, *, cu_q, window=0, sinks=0, scale=0.0, status=None,
+             ws=None, stream=None):
+    """Attention of the tokens q (bf16 [T, Hq, d]) over the cache.  Sequence b
+    has the tokens cu_q[b] : cu_q[b + 1] (int32 [B + 1]), the last of its
+    kv_len[b] (int32 [B]) keys, in the pages table[b] (int32 [B, max_blocks]).
+    out bf16 [T, Hq, d], lse float32 [T, Hq]; window and sinks as in window_attn."""
+    import torch
+    dev = cache.pages.device
+    _need(q.dim() == 3 and table.dim() == 2, "q must have three axes and table two")
+    T, Hq = q.shape[:2]
+    qs = _rows_of(q, "q", T, Hq, cache.d, dev)
+    B, max_blocks = table.shape
+    _same(table, torch.int32, (B, max_blocks), "table", dev)
+    _same(out, torch.bfloat16, (T, Hq, cache.d), "out", dev)
+    if lse is not None:
+        _same(lse, torch.float32, (T, Hq), "lse", dev)
+    if ws is None:
+        ws = workspace(kv4_attn_workspace(cache, Hq), dev)
+    _need(cu_q is not None and kv_len is not None, "cu_q and kv_len are needed")
+    _on(dev, stream, load().sa_kv4_attn, _ptr(q), T, Hq, qs, _index(cu_q, B + 1, "cu_q", dev), B, _ptr(cache.pages),
+        ctypes.byref(cache.desc), _ptr(table), max_blocks, _index(kv_len, B, "kv_len", dev), int(window), int(sinks),
+        float(scale), _ptr(out), _ptr(lse), _index(status, 1, "status", dev), *_ws_args(ws))
+
+
+ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+class Rope:
+    """The frequencies of rotary positions over the first rot_dim channels of
+    a head: base^(-2 i / rot_dim), scaled ("none", "linear", "ntk" or "yarn") for
+    contexts `factor` times the trained one."""
+
+    def __init__(self, rot_dim, *, base=10000.0, layout="half", scaling="none", factor=1.0, original_len=0,
+                 beta_fast=32.0, beta_slow=1.0, device="cuda"):
+        import torch
+        _need(layout in ROPE_LAYOUT, f"layout must be one of {sorted(ROPE_LAYOUT)}")
+        _need(scaling in ROPE_SCALING, f"scaling must be one of {sorted(ROPE_SCALING)}")
+        host = torch.zeros(max(1, int(rot_dim) // 2), dtype=torch.int64)
+        mag = ctypes.c_float()
+        desc = RopeScaling(float(base), float(factor), float(beta_fast), float(beta_slow), int(original_len),
+                           int(rot_dim), ROPE_SCALING[scaling])
+        _check(load().sa_rope_frequencies(ctypes.byref(desc), _ptr(host), ctypes.byref(mag)))
+        self.rot_dim, self.layout = int(rot_dim), ROPE_LAYOUT[layout]
+        self.magnitude = float(mag.value)
+        self.host_freqs = host              # uint64 bits: turns per position in units of 2^-64
+        self.freqs = host.to(device)
+
+
+def _rope_strides(t, name, lead, dtype, dev, d):
+    """Strides {batch, token, head} of a [T, H, d] or [B, N, H, d] tensor."""
+    _same(t, dtype, (*lead, None, d), name, dev, contiguous=False)
+    _need(t.stride(-1) == 1 or d == 1, f"the channels of {name} must be contiguous")
+    s = t.stride()[:-1]
+    return _I64x3(*(s if len(s) == 3 else (0, *s)))
+
+
+def rope(rope: Rope, pos, q, q_out, k=None, k_out=None, *, inverse=False, stream=None):
+    """Rotary positions of the heads q and k ([T, H, d] with pos int32 [T], or
+    [B, N, H, d] with pos [N] or [B, N]; any strides with contiguous channels)
+    into q_out and k_out, which may be q and k.  inverse: turn back, the
+    gradient of the forward rotation."""
+    import torch
+    dev, lead, d = q.device, tuple(q.shape[:-2]), q.shape[-1]
+    _need(len(lead) in (1, 2), "q must have three or four axes")
+    _need((k is None) == (k_out is None), "k and k_out go together")
+    dt = dtype_code(q)
+    qs = _rope_strides(q, "q", lead, q.dtype, dev, d)
+    _same(q_out, q.dtype, tuple(q.shape), "q_out", dev, contiguous=False)
+    qo = _rope_strides(q_out, "q_out", lead, q.dtype, dev, d)
+    ks, ko, Hk = _I64x3(), _I64x3(), 0
+    if k is not None:
+        ks = _rope_strides(k, "k", lead, q.dtype, dev, d)
+        _same(k_out, q.dtype, tuple(k.shape), "k_out", dev, contiguous=False)
+        ko = _rope_strides(k_out, "k_out", lead, q.dtype, dev, d)
+        Hk = k.shape[-2]
+    B, N = (1, lead[0]) if len(lead) == 1 else lead
+    _need(pos.dim() in (1, len(lead)), "pos must be [tokens] or [batch, tokens]")
+    _same(pos, torch.int32, (N,) if pos.dim() == 1 else lead, "pos", dev, contiguous=False)
+    _need(N <= 1 or pos.stride(-1) == 1, "the positions of a sequence must be contiguous")
+    _need(rope.freqs.device == dev, "the frequencies must be on the tensors' device")
+    desc = RopeDesc(B, N, q.shape[-2], Hk, d, qs, qo, ks, ko, pos.stride(0) if pos.dim() == 2 else 0, rope.rot_dim,
+                    rope.layout, dt, int(bool(inverse)), rope.magnitude, 0)
+    _on(dev, stream, load().sa_rope, _ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out), _ptr(pos), _ptr(rope.freqs),
+        ctypes.byref(desc))
+
+
+def cache_plan(kv_len, q_len, table, free_list, free_count, page, new_len, cu_q, slots, positions, free_count_out, *,
+               status=None, stream=None):
+    """One step of a paged cache's bookkeeping, all int32: q_len[b] new tokens
+    (-1: the request ends) of requests with kv_len[b] cached ones.  Updates
+    table [B, max_blocks] and the stack free_list [num_pages] (free_count [1]
+    of them free) in place; writes new_len [B], cu_q [B + 1], slots and
+    positions [max_tokens] and free_count_out [1].  If there are too few pages
+    (status SA_ERR_CAPACITY) nothing changes hands."""
+    import torch
+    dev = table.device
+    _need(table.dim() == 2, "table must have two axes")
+    B, max_blocks = table.shape
+    _same(table, torch.int32, (B, max_blocks), "table", dev)
+    _same(free_list, torch.int32, (None,), "free_list", dev)
+    _same(slots, torch.int32, (None,), "slots", dev)
+    _need(all(t is not None for t in (kv_len, q_len, free_count, new_len, cu_q, positions, free_count_out)),
+          "only status may be None")
+    desc = PlanDesc(B, max_blocks, free_list.numel(), slots.numel(), int(page), 0)
+    _on(dev, stream, load().sa_cache_plan, _index(kv_len, B, "kv_len", dev), _index(q_len, B, "q_len", dev),
+        ctypes.byref(desc), _ptr(table), _ptr(free_list), _index(free_count, 1, "free_count", dev),
+        _index(free_count_out, 1, "free_count_out", dev), _index(new_len, B, "new_len", dev),
+        _index(cu_q, B + 1, "cu_q", dev), _ptr(slots), _index(positions, slots.numel(), "positions", dev),
+        _index(status, 1, "status", dev))
 
 
 # ---------------------------------------------------------------------------
