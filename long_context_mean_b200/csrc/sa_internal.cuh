@@ -220,6 +220,7 @@ struct Kv4AttnArgs {
 };
 size_t decode_ws_bytes(int64_t d);
 sa_status launch_window_decode(const WindowArgs& a, cudaStream_t st);   // bf16, d in {64, 128}
+sa_status launch_window_tc(const WindowArgs& a, cudaStream_t st);       // the same, for many rows
 sa_status launch_window_simt(const WindowArgs& a, cudaStream_t st);     // any dtype and d
 sa_status launch_kv4_attn(const Kv4AttnArgs& a, cudaStream_t st);
 sa_status launch_kv4_append(const void* k, const void* v, int64_t T, const int64_t* ks, const int64_t* vs,

@@ -9,6 +9,7 @@ using namespace sa;
 namespace {
 
 constexpr int64_t kInt32 = INT32_MAX;
+constexpr int64_t kPrefillRows = 64;   // rows of a sequence from which the prefill kernel is used
 
 bool aligned(const void* p, uintptr_t n) { return (uintptr_t)p % n == 0; }
 
@@ -105,7 +106,8 @@ sa_status sa_window_attn(const void* q, const void* k, const void* v, const sa_w
   WindowArgs a{q, k, v, out, lse, q_len, kv_len, status, s, window, sinks,
                scale > 0.f ? scale : 1.0f / std::sqrt((float)s.d), ws};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return on_tensor_cores(s) ? launch_window_decode(a, st) : launch_window_simt(a, st);
+  if (!on_tensor_cores(s)) return launch_window_simt(a, st);
+  return s.Nq >= kPrefillRows ? launch_window_tc(a, st) : launch_window_decode(a, st);
 }
 
 size_t sa_kv4_bytes(const sa_kv4_desc* desc) { return check_kv4(desc) == SA_OK ? kv4_size(*desc) : 0; }

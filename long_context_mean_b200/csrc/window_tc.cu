@@ -1,0 +1,539 @@
+// Prefill attention with a sliding window and first tokens that stay visible,
+// exact to the token, on the sm_100a tensor cores (bf16, d in {64, 128}).
+//
+// Mathematics: row i of a sequence sits at position p = n_k - n_q + i and sees key
+// j iff j <= p, j < n_k and (window == 0 or p - j < window or j < sinks);
+// o = sum 2^(c s_j - m) v_j / l with c = scale log2 e, an online maximum m and the
+// sum l of the same rows.  Only the 128-key tiles that hold a visible pair of a
+// unit are visited: the sinks' tiles and the window's.  Tiles that every row sees
+// whole take no mask.
+//
+// Bound by the tensor cores and the exponentials alike: a 128 x 128 tile of S
+// and its product with V take 1024 clocks of tcgen05.mma, its 16,384
+// exponentials 1024 clocks of the special-function units.  So:
+//  * persistent CTAs, one per SM; a unit is two 128-row query tiles that share
+//    every K and V tile: two query heads of one kv head where the group is even,
+//    two neighbouring row blocks of one head otherwise.  While the softmax of one
+//    tile runs, the tensor cores work on the other.
+//  * tiles of 128 keys: the S product of 128 x 64 x 16 steps would read 6 KB of
+//    shared memory in 32 clocks of mma, above the 128 bytes a clock that an SM
+//    has; 128 x 128 x 16 reads 8 KB in 64.
+//  * warp 0 loads Q and one ring of K and V tiles by TMA, warp 1 issues the
+//    products (S = Q K^T into TMEM, O += P V with P from TMEM over its S), four
+//    warps per query tile do the softmax, one thread a row.  The products of one
+//    query tile are issued in order P V(t), S(t + 1), so S may overwrite P without
+//    a barrier, and S(t + 1)'s arrival tells that P V(t) is done.
+//  * O is rescaled only when a row's maximum grows by more than 2^8.
+// Roundings: P is rounded to bf16 for the second product (l sums the unrounded
+// values); everything else is fp32.
+// V rows that no row of the unit sees (behind a sequence of a padded batch,
+// before the window) are zeroed in shared memory before the product reads them,
+// so that no NaN in them meets a weight of zero.
+// Waits are bounded as in the block-sparse kernel: on expiry SA_ERR_TIMEOUT is
+// raised, every role stops issuing, drains what it issued and leaves.
+#include "sa_internal.cuh"
+#include "tc_ptx.cuh"
+
+namespace sa {
+namespace {
+
+constexpr int kTile = 128;                 // keys of a tile, rows of a query tile
+constexpr int kThreads = 384;              // 4 helper warps, 2 x 4 softmax warps
+constexpr int kStages = 5;                 // K and V tiles in flight
+constexpr float kRescale = 8.0f;           // log2 units
+constexpr unsigned long long kWaitNs = 2000000000ull;
+
+template <int D>
+struct Cfg {
+  static constexpr int CHUNKS = D / 64;               // 128-byte columns of a row
+  static constexpr int TILE_BYTES = kTile * D * 2;
+  static constexpr int CHUNK_BYTES = kTile * 128;
+  static constexpr int OFF_KV = 2 * TILE_BYTES;
+  static constexpr int OFF_CTL = OFF_KV + kStages * TILE_BYTES;
+  static constexpr int SMEM = OFF_CTL + 512 + 1024;   // + alignment slack
+};
+static_assert(Cfg<128>::SMEM <= 227 * 1024, "shared memory above the 227 KB a CTA may use");
+
+struct Ctl {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t kv_full[kStages], kv_empty[kStages];
+  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  uint64_t u_full[4], u_empty[4];
+  uint64_t mma_done;
+  unsigned long long wait_ns;
+  uint32_t tmem_base;
+  volatile uint32_t abort;
+  volatile int32_t ring[4];
+};
+static_assert(sizeof(Ctl) <= 512, "control block too large");
+
+struct Params {
+  uint16_t* out;
+  float* lse;
+  const int32_t* q_len;
+  const int32_t* kv_len;
+  int32_t* status;
+  int32_t* counter;        // next unit past the first of each CTA
+  int32_t B, Hq, Hkv, Nq, Nk, window, sinks;
+  int32_t by_heads;        // the two query tiles are heads (else row blocks)
+  int32_t pairs;           // units of one row block over the batch
+  int32_t num_units;
+  float scale_log2;
+};
+
+// One unit, as every role derives it from its number.
+struct Unit {
+  int32_t bh[2], row0[2];          // the query tiles: head of the batch, first row
+  int32_t first[2], last[2];       // positions of their first and last row
+  bool live[2];
+  int32_t n_q, n_k, kvh;
+  int32_t lo, hi, n_sink;          // keys that some row sees: [0, n_sink) and [lo, hi)
+  int32_t sink_tiles, t_lo, n;     // tiles: the sinks', then from t_lo on
+};
+
+__device__ __forceinline__ Unit unit_at(const Params& p, int i) {
+  Unit u;
+  const int blocks = p.num_units / p.pairs;
+  const int qb = blocks - 1 - i / p.pairs, pair = i % p.pairs;   // the latest rows have the most keys
+  const int per = p.by_heads ? p.Hq / 2 : p.Hq;
+  const int b = pair / per, h = (pair % per) * (p.by_heads ? 2 : 1);
+  u.n_q = p.q_len ? p.q_len[b] : p.Nq;
+  u.n_k = p.kv_len ? p.kv_len[b] : p.Nk;
+  if (u.n_q < 0 || u.n_q > p.Nq || u.n_k < 0 || u.n_k > p.Nk) {
+    raise_status(p.status, SA_ERR_INVALID_ARG);
+    u.n_q = max(0, min(u.n_q, p.Nq));
+    u.n_k = max(0, min(u.n_k, p.Nk));
+  }
+  u.kvh = b * p.Hkv + h / (p.Hq / p.Hkv);
+  int hi = 0;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    u.bh[t] = b * p.Hq + h + (p.by_heads ? t : 0);
+    u.row0[t] = (p.by_heads ? qb : 2 * qb + t) * kTile;
+    u.live[t] = u.row0[t] < u.n_q;
+    u.first[t] = u.n_k - u.n_q + u.row0[t];
+    u.last[t] = u.n_k - u.n_q + min(u.n_q, u.row0[t] + kTile) - 1;
+    if (u.live[t]) hi = max(hi, min(u.n_k, u.last[t] + 1));
+  }
+  u.hi = hi;
+  u.lo = min(p.window ? max(0, u.first[0] - p.window + 1) : 0, hi);
+  u.n_sink = min(p.sinks, u.lo);
+  u.sink_tiles = (u.n_sink + kTile - 1) / kTile;
+  u.t_lo = max(u.sink_tiles, u.lo / kTile);
+  u.n = hi > 0 ? u.sink_tiles + max(0, (hi + kTile - 1) / kTile - u.t_lo) : 0;
+  return u;
+}
+__device__ __forceinline__ int key0(const Unit& u, int t) {
+  return (t < u.sink_tiles ? t : u.t_lo + t - u.sink_tiles) * kTile;
+}
+// Some row of query tile w sees some key of the tile at k0.
+__device__ __forceinline__ bool active(const Params& p, const Unit& u, int w, int k0) {
+  const int hi = min(u.last[w] + 1, u.n_k);
+  const int lo = p.window ? u.first[w] - p.window + 1 : 0;
+  return u.live[w] && (max(k0, lo) < min(k0 + kTile, hi) || k0 < min(p.sinks, hi));
+}
+
+template <int D>
+__device__ void producer(const CUtensorMap* tmQ, const CUtensorMap* tmK, const CUtensorMap* tmV, const Params& p,
+                         Ctl* c, uint32_t sb) {
+  using C = Cfg<D>;
+  uint32_t it = 0, nq[2] = {0, 0};
+  int i = blockIdx.x;
+  auto load = [&](const CUtensorMap* map, int key, int head) {
+    const int s = it % kStages;
+    if (!mbar_wait(&c->kv_empty[s], ((it / kStages) & 1) ^ 1, c, p.status)) return false;
+    mbar_expect_tx(&c->kv_full[s], C::TILE_BYTES);
+#pragma unroll
+    for (int x = 0; x < C::CHUNKS; ++x)
+      tma_load_3d(sb + C::OFF_KV + s * C::TILE_BYTES + x * C::CHUNK_BYTES, map, 64 * x, key, head, &c->kv_full[s]);
+    ++it;
+    return true;
+  };
+  bool ok = true;
+  for (uint32_t j = 0; ok; ++j) {
+    const int slot = j & 3;
+    if (!(ok = mbar_wait(&c->u_empty[slot], ((j >> 2) & 1) ^ 1, c, p.status))) break;
+    if (i >= p.num_units) i = -1;
+    c->ring[slot] = i;
+    mbar_arrive(&c->u_full[slot]);
+    if (i < 0) break;
+    const Unit u = unit_at(p, i);
+    // the next unit: the CTAs' first ones are their own numbers
+    i = p.num_units > (int)gridDim.x ? (int)gridDim.x + atomicAdd(p.counter, 1) : p.num_units;
+    for (int t = 0; t < u.n && ok; ++t) {
+      const int k0 = key0(u, t);
+      if (!(ok = load(tmK, k0, u.kvh))) break;
+      if (t == 0) {
+        for (int w = 0; w < 2 && ok; ++w) {
+          if (!u.live[w]) continue;
+          if (!(ok = mbar_wait(&c->q_empty[w], (nq[w] & 1) ^ 1, c, p.status))) break;
+          ++nq[w];
+          mbar_expect_tx(&c->q_full[w], C::TILE_BYTES);
+#pragma unroll
+          for (int x = 0; x < C::CHUNKS; ++x)
+            tma_load_3d(sb + w * C::TILE_BYTES + x * C::CHUNK_BYTES, tmQ, 64 * x, u.row0[w], u.bh[w], &c->q_full[w]);
+        }
+        if (!ok) break;
+      }
+      ok = load(tmV, k0, u.kvh);
+    }
+  }
+  // The copies issued last have landed before the CTA may exit.
+  for (int w = 0; w < 2; ++w)
+    if (nq[w] > 0) mbar_drain(&c->q_full[w], (nq[w] - 1) & 1, c->wait_ns);
+  for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0; j < it; ++j)
+    mbar_drain(&c->kv_full[j % kStages], (j / kStages) & 1, c->wait_ns);
+}
+
+template <int D>
+__device__ void mma_issuer(const Params& p, Ctl* c, uint32_t sb, uint32_t tm) {
+  using C = Cfg<D>;
+  constexpr uint32_t idesc_s = make_idesc(kTile, kTile, 0), idesc_pv = make_idesc(kTile, D, 1);
+  uint32_t it0 = 0;                                   // ring position of the unit's first K tile
+  uint32_t nq[2] = {0, 0}, np[2] = {0, 0};            // units and tiles so far of each query tile
+  bool ok = true;
+  auto full = [&](uint32_t it) { return mbar_wait(&c->kv_full[it % kStages], (it / kStages) & 1, c, p.status); };
+  for (uint32_t j = 0; ok; ++j) {
+    const int slot = j & 3;
+    if (!(ok = mbar_wait(&c->u_full[slot], (j >> 2) & 1, c, p.status))) break;
+    const int i = c->ring[slot];
+    mbar_arrive(&c->u_empty[slot]);
+    if (i < 0) break;
+    const Unit u = unit_at(p, i);
+    if (u.n == 0) continue;
+    bool some[2] = {false, false};                    // O holds a product of this unit
+    auto qk = [&](int w, int t) {
+      const uint32_t it = it0 + 2 * t;
+      if (!(ok = full(it))) return;
+      tc_fence_after();
+      const uint32_t qbase = sb + w * C::TILE_BYTES, kbase = sb + C::OFF_KV + (it % kStages) * C::TILE_BYTES;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t a = desc_sw128(qbase + (kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32, 16, 1024);
+        const uint64_t b = desc_sw128(kbase + (kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32, 16, 1024);
+        umma_ss(tm + 256 * w + 128, a, b, idesc_s, kk > 0 ? 1u : 0u);
+      }
+      umma_commit(&c->s_full[w]);
+    };
+    if (!(ok = full(it0))) break;
+    for (int w = 0; w < 2 && ok; ++w) {
+      if (!u.live[w]) continue;
+      if (!(ok = mbar_wait(&c->q_full[w], nq[w] & 1, c, p.status))) break;
+      ++nq[w];
+      if (active(p, u, w, key0(u, 0))) qk(w, 0);
+    }
+    if (!ok) break;
+    umma_commit(&c->kv_empty[it0 % kStages]);
+    for (int t = 0; t < u.n && ok; ++t) {
+      const int k0 = key0(u, t), k1 = t + 1 < u.n ? key0(u, t + 1) : 0;
+      const uint32_t itv = it0 + 2 * t + 1;
+      for (int w = 0; w < 2 && ok; ++w) {
+        if (active(p, u, w, k0)) {
+          if (!some[w] && !(ok = mbar_wait(&c->o_free[w], ((nq[w] - 1) & 1) ^ 1, c, p.status))) break;
+          if (!(ok = full(itv))) break;
+          if (!(ok = mbar_wait(&c->p_full[w], np[w] & 1, c, p.status))) break;
+          ++np[w];
+          tc_fence_after();
+          const uint32_t vbase = sb + C::OFF_KV + (itv % kStages) * C::TILE_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            umma_ts(tm + 256 * w, tm + 256 * w + 128 + kk * 8, desc_sw128(vbase + kk * 2048, C::CHUNK_BYTES, 1024),
+                    idesc_pv, some[w] || kk > 0 ? 1u : 0u);
+          some[w] = true;
+        }
+        if (t + 1 < u.n && active(p, u, w, k1)) qk(w, t + 1);
+      }
+      // (waits that are over unless no query tile needed the K or V tile)
+      if (!ok || !(ok = full(itv))) break;
+      umma_commit(&c->kv_empty[itv % kStages]);
+      if (t + 1 < u.n) {
+        if (!(ok = full(itv + 1))) break;
+        umma_commit(&c->kv_empty[(itv + 1) % kStages]);
+      }
+    }
+    for (int w = 0; w < 2 && ok; ++w)
+      if (u.live[w]) {
+        // (one wait a unit, so that the barrier's phases and the units go together)
+        if (!some[w] && !(ok = mbar_wait(&c->o_free[w], ((nq[w] - 1) & 1) ^ 1, c, p.status))) break;
+        umma_commit(&c->q_empty[w]);
+        umma_commit(&c->o_full[w]);
+      }
+    it0 += 2 * u.n;
+  }
+  // Every tensor operation issued here has completed before TMEM is released.
+  umma_commit(&c->mma_done);
+  mbar_drain(&c->mma_done, 0, c->wait_ns);
+}
+
+// Query tile w: thread (quarter wq, lane) owns row 32 wq + lane.
+template <int D>
+__device__ void softmax_rows(const Params& p, Ctl* c, uint8_t* smem, uint32_t tm, int w, int wq, int lane) {
+  using C = Cfg<D>;
+  const int row = wq * 32 + lane;
+  const uint32_t to = tm + 256 * w + ((uint32_t)(wq * 32) << 16), ts = to + 128;
+  const float sc = p.scale_log2;
+  uint32_t it0 = 0, ns = 0, no = 0;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, c, p.status));
+  };
+  for (uint32_t j = 0;; ++j) {
+    const int slot = j & 3;
+    if (!wait(&c->u_full[slot], (j >> 2) & 1)) return;
+    const int i = c->ring[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&c->u_empty[slot]);
+    if (i < 0) return;
+    const Unit u = unit_at(p, i);
+    const int r = u.row0[w] + row;
+    const bool valid = r < u.n_q;
+    const int pos = u.first[w] + row;
+    float m = -INFINITY, l = 0.f;       // the reference maximum (log2 units) and the sum relative to it
+    for (int t = 0; t < u.n; ++t) {
+      const int k0 = key0(u, t);
+      if (!active(p, u, w, k0)) continue;
+      // V rows that no row of the unit sees
+      if (k0 + kTile > u.hi || (k0 < u.lo && k0 + kTile > u.n_sink)) {
+        const uint32_t itv = it0 + 2 * t + 1;
+        if (!wait(&c->kv_full[itv % kStages], (itv / kStages) & 1)) return;
+        const int key = k0 + row;
+        if (key >= u.hi || (key < u.lo && key >= u.n_sink)) {
+          // the swizzle moves 16-byte pieces within a row's 128 bytes: the whole row is zeroed
+          uint4* v = reinterpret_cast<uint4*>(smem + C::OFF_KV + (itv % kStages) * C::TILE_BYTES + row * 128);
+#pragma unroll
+          for (int x = 0; x < C::CHUNKS; ++x)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[x * (C::CHUNK_BYTES / 16) + e] = make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      if (!wait(&c->s_full[w], ns & 1)) return;
+      ++ns;
+      tc_fence_after();
+      float s[kTile];
+#pragma unroll
+      for (int x = 0; x < kTile / 32; ++x) tmem_ld32(ts + x * 32, s + x * 32);
+      tmem_wait_ld();
+      const bool whole = k0 + kTile - 1 <= u.first[w] && k0 + kTile <= u.n_k &&
+                         (p.window == 0 || u.last[w] - k0 < p.window || k0 + kTile <= p.sinks);
+      if (!whole) {
+        const int c_hi = min(pos, u.n_k - 1) - k0, c_lo = p.window ? pos - p.window + 1 - k0 : 0, c_s = p.sinks - k0;
+#pragma unroll
+        for (int x = 0; x < kTile; ++x)
+          if (x > c_hi || (x < c_lo && x >= c_s)) s[x] = -INFINITY;
+      }
+      float mx[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) mx[x] = fmaxf(s[x], s[x + 4]);
+#pragma unroll
+      for (int x = 8; x < kTile; x += 8)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) mx[y] = max3(mx[y], s[x + y], s[x + y + 4]);
+      const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sc;
+      float corr = 1.f;
+      bool moved = false;
+      if (top > m + kRescale || (m == -INFINITY && top > m)) {
+        moved = m != -INFINITY;         // (a row that saw nothing so far has O = 0)
+        corr = ex2(m - top);
+        m = top;
+      }
+      const float ref = m == -INFINITY ? 0.f : m;
+      const uint64_t sc2 = pack2(sc, sc), neg2 = pack2(-ref, -ref);
+      uint64_t acc[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) acc[x] = pack2(0.f, 0.f);
+      // O's rescale first: S(t)'s arrival tells that P V of the tile before is done.
+      if (__any_sync(0xffffffffu, moved)) {
+        const float f = moved ? corr : 1.f;
+#pragma unroll 1
+        for (int x = 0; x < D / 32; ++x) {
+          float o[32];
+          tmem_ld32(to + x * 32, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] *= f;
+          tmem_st32(to + x * 32, reinterpret_cast<const uint32_t*>(o));
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          float a, b;
+          unpack2(ffma2(pack2(s[64 * x + 2 * e], s[64 * x + 2 * e + 1]), sc2, neg2), a, b);
+          a = ex2(a);
+          b = ex2(b);
+          acc[e & 3] = fadd2(acc[e & 3], pack2(a, b));
+          pk[e] = pack_bf16(a, b);
+        }
+        tmem_st32(ts + x * 32, pk);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->p_full[w]);
+      float a, b;
+      unpack2(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), a, b);
+      l = l * corr + (a + b);
+    }
+    it0 += 2 * u.n;
+    if (!u.live[w]) continue;
+    const bool product = u.n > 0;
+    if (product) {
+      if (!wait(&c->o_full[w], no & 1)) return;
+      ++no;
+      tc_fence_after();
+    }
+    const float inv = 1.f / l;
+    uint16_t* orow = p.out + ((int64_t)u.bh[w] * p.Nq + r) * D;
+#pragma unroll 1
+    for (int x = 0; x < D / 32; ++x) {
+      float o[32];
+      if (product) {
+        tmem_ld32(to + x * 32, o);
+        tmem_wait_ld();
+      }
+      if (!valid) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint4 v = make_uint4(0, 0, 0, 0);   // a row that sees no key
+        if (l != 0.f) {
+          v.x = pack_bf16(o[8 * e + 0] * inv, o[8 * e + 1] * inv);
+          v.y = pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv);
+          v.z = pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv);
+          v.w = pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv);
+        }
+        *reinterpret_cast<uint4*>(orow + x * 32 + e * 8) = v;
+      }
+    }
+    if (product) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->o_free[w]);
+    }
+    if (valid && p.lse) p.lse[(int64_t)u.bh[w] * p.Nq + r] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_u32(smem);
+  Ctl* c = reinterpret_cast<Ctl*>(smem + C::OFF_CTL);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&c->q_full[w], 1);
+      mbar_init(&c->q_empty[w], 1);
+      mbar_init(&c->s_full[w], 1);
+      mbar_init(&c->p_full[w], 4);    // one lane of each softmax warp
+      mbar_init(&c->o_full[w], 1);
+      mbar_init(&c->o_free[w], 4);
+    }
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&c->kv_full[s], 1);
+      mbar_init(&c->kv_empty[s], 1);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&c->u_full[s], 1);
+      mbar_init(&c->u_empty[s], 9);   // the MMA lane and one lane of each softmax warp
+    }
+    mbar_init(&c->mma_done, 1);
+    c->wait_ns = kWaitNs;
+    c->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&c->tmem_base)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c->tmem_base;
+
+  // 384 x 168 registers at launch; 256 x 216 + 128 x 64 fit in them.
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 0 && lane == 0) producer<D>(&tmQ, &tmK, &tmV, p, c, sb);
+    if (warp == 1 && lane == 0) mma_issuer<D>(p, c, sb, tmem);
+    __syncwarp();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    softmax_rows<D>(p, c, smem, tmem, (warp - 4) >> 2, warp & 3, lane);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+}
+
+// 3-D map over [heads][N][D] bf16, box [1][128][64], 128-byte swizzle.
+bool make_map(CUtensorMap* m, const void* base, int64_t heads, int64_t N, int D) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)heads};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)N * D * 2};
+  cuuint32_t box[3] = {64, kTile, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+sa_status launch(const WindowArgs& x, cudaStream_t st) {
+  using C = Cfg<D>;
+  const sa_window_shape& s = x.shape;
+  CUtensorMap mq, mk, mv;
+  if (!make_map(&mq, x.q, s.B * s.Hq, s.Nq, D) || !make_map(&mk, x.k, s.B * s.Hkv, s.Nk, D) ||
+      !make_map(&mv, x.v, s.B * s.Hkv, s.Nk, D))
+    return set_error(SA_ERR_CUDA, "cuTensorMapEncodeTiled failed (driver entry point unavailable or bad map)");
+  Params p{};
+  p.out = static_cast<uint16_t*>(x.out);
+  p.lse = x.lse;
+  p.q_len = x.q_len;
+  p.kv_len = x.kv_len;
+  p.status = x.status;
+  p.counter = static_cast<int32_t*>(x.ws);
+  p.B = (int32_t)s.B;
+  p.Hq = (int32_t)s.Hq;
+  p.Hkv = (int32_t)s.Hkv;
+  p.Nq = (int32_t)s.Nq;
+  p.Nk = (int32_t)s.Nk;
+  // a window that reaches past every key is none; so no position minus window leaves 31 bits
+  p.window = x.window >= s.Nk ? 0 : (int32_t)x.window;
+  p.sinks = (int32_t)min64(x.sinks, s.Nk);
+  p.by_heads = (s.Hq / s.Hkv) % 2 == 0;
+  const int64_t tiles = ceil_div(s.Nq, kTile);
+  const int64_t pairs = s.B * (p.by_heads ? s.Hq / 2 : s.Hq), units = pairs * (p.by_heads ? tiles : ceil_div(tiles, 2));
+  if (units > INT32_MAX / 2) return set_error(SA_ERR_UNSUPPORTED, "too many rows");
+  p.pairs = (int32_t)pairs;
+  p.num_units = (int32_t)units;
+  p.scale_log2 = x.scale * kLog2e;
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (cudaFuncSetAttribute(window_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    return set_error(SA_ERR_CUDA, "cudaFuncSetAttribute(window_tc_kernel) failed");
+  if (units > sms && cudaMemsetAsync(p.counter, 0, sizeof(int32_t), st) != cudaSuccess)
+    return set_error(SA_ERR_CUDA, "cudaMemsetAsync(work counter) failed");
+  window_tc_kernel<D><<<(unsigned)min64(units, sms), kThreads, C::SMEM, st>>>(mq, mk, mv, p);
+  return check_launch("window_tc_kernel");
+}
+
+}  // namespace
+
+sa_status launch_window_tc(const WindowArgs& a, cudaStream_t st) {
+  return a.shape.d == 128 ? launch<128>(a, st) : launch<64>(a, st);
+}
+
+}  // namespace sa

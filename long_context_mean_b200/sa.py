@@ -442,37 +442,51 @@ def _need(ok, msg):
 
 
 def _same(t, dtype, shape, name, device, contiguous=True):
-    """t is a CUDA tensor of this dtype, shape (None entries: any) and device."""
+    """t is a CUDA tensor of this dtype, shape and device.  (The messages are
+    built only for a tensor that is refused: a step of single tokens makes
+    some thirty of these checks.)"""
     import torch
-    _need(isinstance(t, torch.Tensor) and t.dtype == dtype, f"{name} must be a {dtype} tensor")
-    _need(t.device == device and t.is_cuda, f"{name} must be on the same CUDA device as the other tensors")
-    _need(t.dim() == len(shape) and all(w is None or n == w for n, w in zip(t.shape, shape)),
-          f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    _need(not contiguous or t.is_contiguous(), f"{name} must be contiguous")
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype):
+        raise ValueError(f"{name} must be a {dtype} tensor")
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{name} must be on the same CUDA device as the other tensors")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
 def _index(t, n, name, device):
-    """An int32 [n] argument, or None."""
+    """The address of an int32 [n] argument, or None."""
+    if t is None:
+        return None
     import torch
-    if t is not None:
-        _same(t, torch.int32, (n,), name, device)
-    return _ptr(t)
+    _same(t, torch.int32, (n,), name, device)
+    return t.data_ptr()
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _on(device, stream, fn, *args):
     """fn(*args, stream) with `device` current."""
     import torch
     if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)))
+        s = torch.cuda.current_stream() if stream is None else stream
+        code = fn(*args, s.cuda_stream)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, _stream(stream)))
+            s = torch.cuda.current_stream() if stream is None else stream
+            code = fn(*args, s.cuda_stream)
+    if code != SA_OK:
+        _check(code)
 
 
 def _ws_args(ws):
-    import torch
-    _need(isinstance(ws, torch.Tensor) and ws.is_contiguous(), "ws must be a contiguous tensor")
-    return _ptr(ws), ws.numel() * ws.element_size()
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def make_window_shape(q, k) -> WindowShape:
@@ -497,18 +511,19 @@ def window_attn(q, k, v, out, lse=None, *, window=0, sinks=0, q_len=None, kv_len
     dev = q.device
     _need(q.dim() == 4 and k.dim() == 4, "q and k must have four axes")
     B, Hq, Nq, d = q.shape
+    Hkv, Nk = k.shape[1:3]
     _same(q, q.dtype, (B, Hq, Nq, d), "q", dev)
-    _same(k, q.dtype, (B, None, None, d), "k", dev)
-    _same(v, q.dtype, tuple(k.shape), "v", dev)
-    _same(out, q.dtype, tuple(q.shape), "out", dev)
+    _same(k, q.dtype, (B, Hkv, Nk, d), "k", dev)
+    _same(v, q.dtype, (B, Hkv, Nk, d), "v", dev)
+    _same(out, q.dtype, (B, Hq, Nq, d), "out", dev)
     if lse is not None:
         _same(lse, torch.float32, (B, Hq, Nq), "lse", dev)
-    shape = make_window_shape(q, k)
+    shape = WindowShape(B, Hq, Hkv, Nq, Nk, d, dtype_code(q), 0)
     if ws is None:
         ws = workspace(load().sa_window_attn_workspace(ctypes.byref(shape)), dev)
-    _on(dev, stream, load().sa_window_attn, _ptr(q), _ptr(k), _ptr(v), ctypes.byref(shape), int(window), int(sinks),
-        _index(q_len, B, "q_len", dev), _index(kv_len, B, "kv_len", dev), float(scale), _ptr(out), _ptr(lse),
-        _index(status, 1, "status", dev), *_ws_args(ws))
+    _on(dev, stream, load().sa_window_attn, q.data_ptr(), k.data_ptr(), v.data_ptr(), ctypes.byref(shape), int(window),
+        int(sinks), _index(q_len, B, "q_len", dev), _index(kv_len, B, "kv_len", dev), float(scale), out.data_ptr(),
+        _at(lse), _index(status, 1, "status", dev), *_ws_args(ws))
 
 
 class KV4Cache:
@@ -518,7 +533,7 @@ class KV4Cache:
     def __init__(self, pages, page: int, d: int):
         import torch
         _need(pages.dim() == 4, "the pages must have four axes")
-        _same(pages, torch.uint8, (None, None, page // 16, 18 * d), "pages", pages.device)
+        _same(pages, torch.uint8, (*pages.shape[:2], page // 16, 18 * d), "pages", pages.device)
         self.pages, self.page, self.d = pages, int(page), int(d)
         self.num_pages, self.Hkv = pages.shape[:2]
         self.desc = KV4Desc(self.num_pages, self.Hkv, self.page, self.d)
@@ -531,23 +546,26 @@ class KV4Cache:
         return cls(torch.zeros(num_pages, Hkv, page // 16, 18 * d, dtype=torch.uint8, device=device), page, d)
 
 
-_I64x2, _I64x3 = ctypes.c_int64 * 2, ctypes.c_int64 * 3
+_I64x2 = ctypes.c_int64 * 2
 
 
 def _rows_of(t, name, T, H, d, dev):
+    """Strides {token, head} of a bf16 [T, H, d] tensor."""
     import torch
     _same(t, torch.bfloat16, (T, H, d), name, dev, contiguous=False)
-    _need(d == 1 or t.stride(2) == 1, f"the channels of {name} must be contiguous")
-    return ctypes.byref(_I64x2(t.stride(0), t.stride(1)))
+    s = t.stride()
+    if s[2] != 1 and d != 1:
+        raise ValueError(f"the channels of {name} must be contiguous")
+    return ctypes.byref(_I64x2(s[0], s[1]))
 
 
 def kv4_append(k, v, slots, cache: KV4Cache, *, status=None, stream=None):
     """Tokens k, v (bf16 [T, Hkv, d]) into the slots of the cache (int32 [T],
     -1 = leave out; the others must differ)."""
     T, dev = k.shape[0], cache.pages.device
-    ks, vs = (_rows_of(t, n, T, cache.Hkv, cache.d, dev) for t, n in ((k, "k"), (v, "v")))
-    _on(dev, stream, load().sa_kv4_append, _ptr(k), _ptr(v), T, ks, vs, _index(slots, T, "slots", dev),
-        ctypes.byref(cache.desc), _ptr(cache.pages), _index(status, 1, "status", dev))
+    ks, vs = _rows_of(k, "k", T, cache.Hkv, cache.d, dev), _rows_of(v, "v", T, cache.Hkv, cache.d, dev)
+    _on(dev, stream, load().sa_kv4_append, k.data_ptr(), v.data_ptr(), T, ks, vs, _index(slots, T, "slots", dev),
+        ctypes.byref(cache.desc), cache.pages.data_ptr(), _index(status, 1, "status", dev))
 
 
 def kv4_read(cache: KV4Cache, slots, k, v, *, status=None, stream=None):
@@ -556,8 +574,8 @@ def kv4_read(cache: KV4Cache, slots, k, v, *, status=None, stream=None):
     T, dev = k.shape[0], cache.pages.device
     _same(k, torch.bfloat16, (T, cache.Hkv, cache.d), "k", dev)
     _same(v, torch.bfloat16, (T, cache.Hkv, cache.d), "v", dev)
-    _on(dev, stream, load().sa_kv4_read, _ptr(cache.pages), ctypes.byref(cache.desc), _index(slots, T, "slots", dev), T,
-        _ptr(k), _ptr(v), _index(status, 1, "status", dev))
+    _on(dev, stream, load().sa_kv4_read, cache.pages.data_ptr(), ctypes.byref(cache.desc),
+        _index(slots, T, "slots", dev), T, k.data_ptr(), v.data_ptr(), _index(status, 1, "status", dev))
 
 
 def kv4_attn_workspace(cache: KV4Cache, Hq: int) -> int:
@@ -584,9 +602,10 @@ def kv4_attn(q, cache: KV4Cache, table, kv_len, out, lse=None, *, cu_q, window=0
     if ws is None:
         ws = workspace(kv4_attn_workspace(cache, Hq), dev)
     _need(cu_q is not None and kv_len is not None, "cu_q and kv_len are needed")
-    _on(dev, stream, load().sa_kv4_attn, _ptr(q), T, Hq, qs, _index(cu_q, B + 1, "cu_q", dev), B, _ptr(cache.pages),
-        ctypes.byref(cache.desc), _ptr(table), max_blocks, _index(kv_len, B, "kv_len", dev), int(window), int(sinks),
-        float(scale), _ptr(out), _ptr(lse), _index(status, 1, "status", dev), *_ws_args(ws))
+    _on(dev, stream, load().sa_kv4_attn, q.data_ptr(), T, Hq, qs, _index(cu_q, B + 1, "cu_q", dev), B,
+        cache.pages.data_ptr(), ctypes.byref(cache.desc), table.data_ptr(), max_blocks,
+        _index(kv_len, B, "kv_len", dev), int(window), int(sinks), float(scale), out.data_ptr(), _at(lse),
+        _index(status, 1, "status", dev), *_ws_args(ws))
 
 
 ROPE_LAYOUT = {"half": 0, "interleaved": 1}
@@ -614,12 +633,13 @@ class Rope:
         self.freqs = host.to(device)
 
 
-def _rope_strides(t, name, lead, dtype, dev, d):
+def _rope_strides(t, name, shape, dtype, dev):
     """Strides {batch, token, head} of a [T, H, d] or [B, N, H, d] tensor."""
-    _same(t, dtype, (*lead, None, d), name, dev, contiguous=False)
-    _need(t.stride(-1) == 1 or d == 1, f"the channels of {name} must be contiguous")
-    s = t.stride()[:-1]
-    return _I64x3(*(s if len(s) == 3 else (0, *s)))
+    _same(t, dtype, shape, name, dev, contiguous=False)
+    s = t.stride()
+    if s[-1] != 1 and shape[-1] != 1:
+        raise ValueError(f"the channels of {name} must be contiguous")
+    return s[:3] if len(s) == 4 else (0, s[0], s[1])
 
 
 def rope(rope: Rope, pos, q, q_out, k=None, k_out=None, *, inverse=False, stream=None):
@@ -628,28 +648,26 @@ def rope(rope: Rope, pos, q, q_out, k=None, k_out=None, *, inverse=False, stream
     into q_out and k_out, which may be q and k.  inverse: turn back, the
     gradient of the forward rotation."""
     import torch
-    dev, lead, d = q.device, tuple(q.shape[:-2]), q.shape[-1]
-    _need(len(lead) in (1, 2), "q must have three or four axes")
+    dev, shape, dt = q.device, q.shape, q.dtype
+    _need(len(shape) in (3, 4), "q must have three or four axes")
     _need((k is None) == (k_out is None), "k and k_out go together")
-    dt = dtype_code(q)
-    qs = _rope_strides(q, "q", lead, q.dtype, dev, d)
-    _same(q_out, q.dtype, tuple(q.shape), "q_out", dev, contiguous=False)
-    qo = _rope_strides(q_out, "q_out", lead, q.dtype, dev, d)
-    ks, ko, Hk = _I64x3(), _I64x3(), 0
+    lead, d = shape[:-2], shape[-1]
+    qs, qo = _rope_strides(q, "q", shape, dt, dev), _rope_strides(q_out, "q_out", shape, dt, dev)
+    ks = ko = (0, 0, 0)
+    Hk = 0
     if k is not None:
-        ks = _rope_strides(k, "k", lead, q.dtype, dev, d)
-        _same(k_out, q.dtype, tuple(k.shape), "k_out", dev, contiguous=False)
-        ko = _rope_strides(k_out, "k_out", lead, q.dtype, dev, d)
         Hk = k.shape[-2]
+        ks = _rope_strides(k, "k", (*lead, Hk, d), dt, dev)
+        ko = _rope_strides(k_out, "k_out", (*lead, Hk, d), dt, dev)
     B, N = (1, lead[0]) if len(lead) == 1 else lead
-    _need(pos.dim() in (1, len(lead)), "pos must be [tokens] or [batch, tokens]")
-    _same(pos, torch.int32, (N,) if pos.dim() == 1 else lead, "pos", dev, contiguous=False)
+    batched = pos.dim() == 2 and len(lead) == 2
+    _same(pos, torch.int32, lead if batched else (N,), "pos", dev, contiguous=False)
     _need(N <= 1 or pos.stride(-1) == 1, "the positions of a sequence must be contiguous")
     _need(rope.freqs.device == dev, "the frequencies must be on the tensors' device")
-    desc = RopeDesc(B, N, q.shape[-2], Hk, d, qs, qo, ks, ko, pos.stride(0) if pos.dim() == 2 else 0, rope.rot_dim,
-                    rope.layout, dt, int(bool(inverse)), rope.magnitude, 0)
-    _on(dev, stream, load().sa_rope, _ptr(q), _ptr(q_out), _ptr(k), _ptr(k_out), _ptr(pos), _ptr(rope.freqs),
-        ctypes.byref(desc))
+    desc = RopeDesc(B, N, shape[-2], Hk, d, qs, qo, ks, ko, pos.stride(0) if batched else 0, rope.rot_dim, rope.layout,
+                    dtype_code(q), int(bool(inverse)), rope.magnitude, 0)
+    _on(dev, stream, load().sa_rope, q.data_ptr(), q_out.data_ptr(), _at(k), _at(k_out), pos.data_ptr(),
+        rope.freqs.data_ptr(), ctypes.byref(desc))
 
 
 def cache_plan(kv_len, q_len, table, free_list, free_count, page, new_len, cu_q, slots, positions, free_count_out, *,
@@ -664,16 +682,16 @@ def cache_plan(kv_len, q_len, table, free_list, free_count, page, new_len, cu_q,
     dev = table.device
     _need(table.dim() == 2, "table must have two axes")
     B, max_blocks = table.shape
+    num_pages, max_tokens = free_list.numel(), slots.numel()
     _same(table, torch.int32, (B, max_blocks), "table", dev)
-    _same(free_list, torch.int32, (None,), "free_list", dev)
-    _same(slots, torch.int32, (None,), "slots", dev)
-    _need(all(t is not None for t in (kv_len, q_len, free_count, new_len, cu_q, positions, free_count_out)),
-          "only status may be None")
-    desc = PlanDesc(B, max_blocks, free_list.numel(), slots.numel(), int(page), 0)
+    _need(not any(t is None for t in (kv_len, q_len, free_list, free_count, new_len, cu_q, slots, positions,
+                                      free_count_out)), "only status may be None")
+    desc = PlanDesc(B, max_blocks, num_pages, max_tokens, int(page), 0)
     _on(dev, stream, load().sa_cache_plan, _index(kv_len, B, "kv_len", dev), _index(q_len, B, "q_len", dev),
-        ctypes.byref(desc), _ptr(table), _ptr(free_list), _index(free_count, 1, "free_count", dev),
-        _index(free_count_out, 1, "free_count_out", dev), _index(new_len, B, "new_len", dev),
-        _index(cu_q, B + 1, "cu_q", dev), _ptr(slots), _index(positions, slots.numel(), "positions", dev),
+        ctypes.byref(desc), table.data_ptr(), _index(free_list, num_pages, "free_list", dev),
+        _index(free_count, 1, "free_count", dev), _index(free_count_out, 1, "free_count_out", dev),
+        _index(new_len, B, "new_len", dev), _index(cu_q, B + 1, "cu_q", dev),
+        _index(slots, max_tokens, "slots", dev), _index(positions, max_tokens, "positions", dev),
         _index(status, 1, "status", dev))
 
 
