@@ -15,8 +15,9 @@
 //    units (sequence, row tile, kv head) and a unit several pieces.  Units that
 //    lie in one piece are finished there; parts of others go to the workspace
 //    and join_kernel adds them up in a fixed order (no atomics).
-//  * each warp streams its own tiles through its own ring of cp.async stages
-//    (no block barrier in the loop) and multiplies with mma.sync m16n8k16: the
+//  * each warp streams its own tiles through its own ring of stages (bulk
+//    copies for the cache's subtiles, cp.async for rows; no block barrier in
+//    the loop) and multiplies with mma.sync m16n8k16: the
 //    16 side is the tokens (K) or channels (V), the 8 side the query rows, so a
 //    group of 8 rows wastes nothing.  (tcgen05 wants its operands in shared
 //    memory: the widened codes would have to be written there, 4 times the bytes
@@ -41,9 +42,8 @@ constexpr int kJoinThreads = 256;
 
 // What a worker leaves for join_kernel.
 struct Piece {
-  int32_t has_head, head_ends;    // its first part belongs to a unit that began in an earlier piece
-  int32_t has_tail;               // its last part begins a unit that a later piece ends
-  int32_t b, row0, kvh, pad0, pad1;   // that unit
+  int32_t last;          // the piece that ends the unit which begins in this one and goes on past it; 0: none
+  int32_t b, row0, kvh;  // that unit
 };
 
 struct DecodeArgs {
@@ -64,8 +64,8 @@ struct DecodeArgs {
   int64_t q_sb, q_st, q_sh;      // element strides of q: sequence, token, head
   int64_t o_sb, o_st, o_sh;      // of out (lse: the same / d)
   int64_t T, Nq, Nk;             // packed tokens; tokens and keys per sequence at most
-  int64_t max_blocks, num_pages;
-  int64_t window, sinks;
+  int64_t max_blocks;
+  int32_t num_pages, window, sinks;
   int32_t B, Hkv, group, lg_page;
   float scale_log2;
 };
@@ -83,6 +83,40 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// mbarriers of a warp's stages (arrivals: the fetching lanes) and bulk copies.
+__device__ __forceinline__ void bar_init(uint32_t bar, int n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, int bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, int bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok)
+               : "r"(bar), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+// Bounded wait for a copy in flight (2 s; a copy always arrives, so the bound
+// only keeps a broken device from holding the kernel).
+__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, int32_t* status) {
+  if (bar_try(bar, parity)) return;
+  unsigned long long t0, t1;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+  while (!bar_try(bar, parity)) {
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t1));
+    if (t1 - t0 > 2000000000ull) {
+      raise_status(status, SA_ERR_TIMEOUT);
+      return;
+    }
+  }
+}
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -111,54 +145,46 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w) {
 }
 
 // One unit: a sequence's row tile on one kv head, and the tiles it visits.
+// (Tokens and keys of a sequence fit 30 bits.)
 struct Unit {
-  int64_t b, n_k, n_q, q0;         // sequence, its keys and rows' tokens, first packed token
-  int64_t lo, hi, n_sink;          // keys [0, n_sink) and [lo, hi) are visited
+  int32_t b, n_k, n_q, q0;         // sequence, its keys and rows' tokens, first packed token
+  int32_t lo, n_sink;              // keys [0, n_sink) and [lo, n_k) are visited
+  int32_t sink_tiles, t_lo;        // the sinks' tiles, then those from t_lo on
   int32_t row0, kvh;
 };
 
 // Sequence b as the whole batch sees it: tokens, keys, row tiles and tiles.
 template <int TOK, int ROWS>
-__device__ __forceinline__ void sequence(const DecodeArgs& a, int64_t b, Unit& u, int64_t& row_tiles, int64_t& tiles) {
+__device__ __forceinline__ void sequence(const DecodeArgs& a, int b, Unit& u, int& row_tiles, int& tiles) {
+  const int T = (int)a.T, Nq = (int)a.Nq, Nk = (int)a.Nk;
   u.b = b;
+  bool bad = false;
   if (a.cu_q) {
-    int64_t c0 = a.cu_q[b], c1 = a.cu_q[b + 1];
-    if (c0 < 0 || c1 < c0 || c1 > a.T) {
-      raise_status(a.status, SA_ERR_INVALID_ARG);
-      c0 = max64(0, min64(c0, a.T));
-      c1 = max64(c0, min64(c1, a.T));
-    }
+    int c0 = a.cu_q[b], c1 = a.cu_q[b + 1];
+    bad = c0 < 0 || c1 < c0 || c1 > T;
+    c0 = max(0, min(c0, T));
+    c1 = max(c0, min(c1, T));
     u.q0 = c0;
     u.n_q = c1 - c0;
   } else {
     u.q0 = 0;
-    u.n_q = a.q_len ? a.q_len[b] : a.Nq;
-    if (u.n_q < 0 || u.n_q > a.Nq) {
-      raise_status(a.status, SA_ERR_INVALID_ARG);
-      u.n_q = max64(0, min64(u.n_q, a.Nq));
-    }
+    const int n = a.q_len ? a.q_len[b] : Nq;
+    u.n_q = max(0, min(n, Nq));
+    bad = n != u.n_q;
   }
-  u.n_k = a.kv_len ? a.kv_len[b] : a.Nk;
-  if (u.n_k < 0 || u.n_k > a.Nk) {
-    raise_status(a.status, SA_ERR_INVALID_ARG);
-    u.n_k = max64(0, min64(u.n_k, a.Nk));
-  }
-  const int64_t first = u.n_k - u.n_q;    // position of the first row
-  u.hi = u.n_k;
-  u.lo = a.window > 0 ? max64(0, first - a.window + 1) : 0;
-  u.lo = min64(u.lo, u.hi);
-  u.n_sink = min64(min64(a.sinks, u.lo), u.hi);
+  const int n = a.kv_len ? a.kv_len[b] : Nk;
+  u.n_k = max(0, min(n, Nk));
+  if (bad || n != u.n_k) raise_status(a.status, SA_ERR_INVALID_ARG);
+  const int first = u.n_k - u.n_q;    // position of the first row
+  u.lo = min(a.window > 0 ? max(0, first - a.window + 1) : 0, u.n_k);
+  u.n_sink = min(a.sinks, u.lo);
   // whole tiles; the window's tiles start behind the sinks' tiles
-  const int64_t st = ceil_div_d(u.n_sink, TOK);
-  const int64_t t0 = max64(st, u.lo / TOK);
-  tiles = max64(1, st + max64(0, ceil_div_d(u.hi, TOK) - t0));
+  u.sink_tiles = (u.n_sink + TOK - 1) / TOK;
+  u.t_lo = max(u.sink_tiles, u.lo / TOK);
+  tiles = max(1, u.sink_tiles + max(0, (u.n_k + TOK - 1) / TOK - u.t_lo));
   row_tiles = u.n_q > 0 ? (u.n_q * a.group + ROWS - 1) / ROWS : 0;
 }
-template <int TOK>
-__device__ __forceinline__ int64_t tile_at(const Unit& u, int64_t i) {
-  const int64_t st = ceil_div_d(u.n_sink, TOK);
-  return i < st ? i : max64(st, u.lo / TOK) + (i - st);
-}
+__device__ __forceinline__ int tile_at(const Unit& u, int i) { return i < u.sink_tiles ? i : u.t_lo + (i - u.sink_tiles); }
 
 // ---------------------------------------------------------------------------
 // Formats: how a tile is fetched and multiplied
@@ -184,38 +210,31 @@ struct Kv4 {
       q[4 * g + 3] = __byte_perm(w.y, w.w, 0x7632);
     }
   }
-  int32_t page[SUBS];   // table entries of the tile that is fetched next; kSkip: no row sees the subtile
+  // Lane s < SUBS looks up and fetches subtile s: one bulk copy of its bytes,
+  // which the stage's mbarrier counts.  A subtile that no row sees is left
+  // out: its stage holds old bytes, whose scores are masked and whose scales are
+  // replaced by zero.
+  static constexpr bool kBulk = true;
   static constexpr int32_t kSkip = INT32_MIN;
-  __device__ __forceinline__ void look(const DecodeArgs& a, const Unit& u, int64_t t0) {
-#pragma unroll
-    for (int s = 0; s < SUBS; ++s) {
-      const int64_t at = t0 + 16 * s;
-      const bool seen = at < u.n_k && (at + 16 > u.lo || at < u.n_sink);
-      page[s] = seen ? max(-1, a.table[u.b * a.max_blocks + (at >> a.lg_page)]) : kSkip;
-    }
+  int32_t page = kSkip;   // table entry of the tile that is fetched next
+  __device__ __forceinline__ void look(const DecodeArgs& a, const Unit& u, int t0, int lane) {
+    const int at = t0 + 16 * lane;
+    const bool seen = lane < SUBS && at < u.n_k && (at + 16 > u.lo || at < u.n_sink);
+    page = seen ? max(-1, a.table[(int64_t)u.b * a.max_blocks + (at >> a.lg_page)]) : kSkip;
   }
-  // (The stage of a subtile that is left out holds old bytes: their scores are
-  // masked and their scales replaced by zero.)
-  __device__ __forceinline__ void fetch(const DecodeArgs& a, const Unit& u, int64_t t0, uint32_t dst, int lane) {
-#pragma unroll
-    for (int s = 0; s < SUBS; ++s) {
-      if (page[s] == kSkip) continue;
-      const int64_t at = t0 + 16 * s;
-      int64_t pg = page[s];
-      if (pg < 0 || pg >= a.num_pages) {   // the sequence's result is not defined, the access stays inside
-        if (lane == 0) raise_status(a.status, SA_ERR_INVALID_ARG);
-        pg = 0;
-      }
-      const int in = (int)(at & ((1 << a.lg_page) - 1)) >> 4;
-      const uint8_t* src = a.cache + (((pg * a.Hkv + u.kvh) << (a.lg_page - 4)) + in) * (int64_t)SUB_BYTES;
-#pragma unroll
-      for (int i = 0; i < SUB_BYTES / 512; ++i) cp16(dst + s * SUB_BYTES + (i * 32 + lane) * 16, src + (i * 32 + lane) * 16, true);
-      constexpr int rest = SUB_BYTES % 512 / 16;
-      if (rest && lane < rest) {
-        constexpr int o = SUB_BYTES / 512 * 512;
-        cp16(dst + s * SUB_BYTES + o + lane * 16, src + o + lane * 16, true);
-      }
+  __device__ __forceinline__ void fetch(const DecodeArgs& a, const Unit& u, int t0, uint32_t dst, uint32_t bar, int lane) {
+    if (lane >= SUBS) return;
+    const bool seen = page != kSkip;
+    bar_expect(bar, seen ? SUB_BYTES : 0);
+    if (!seen) return;
+    int pg = page;
+    if (pg < 0 || pg >= a.num_pages) {   // the sequence's result is not defined, the access stays inside
+      raise_status(a.status, SA_ERR_INVALID_ARG);
+      pg = 0;
     }
+    const int in = ((t0 + 16 * lane) & ((1 << a.lg_page) - 1)) >> 4;
+    bulk_load(dst + lane * SUB_BYTES, a.cache + ((((int64_t)pg * a.Hkv + u.kvh) << (a.lg_page - 4)) + in) * SUB_BYTES,
+              SUB_BYTES, bar);
   }
   template <int NQ>
   static __device__ __forceinline__ void scores(const uint8_t* st, int s, const uint32_t (*q)[QREGS], int lane, float (*out)[4]) {
@@ -308,13 +327,14 @@ struct Bf16 {
       q[4 * c + 3] = w.w;
     }
   }
-  __device__ __forceinline__ void look(const DecodeArgs&, const Unit&, int64_t) {}
-  __device__ __forceinline__ void fetch(const DecodeArgs& a, const Unit& u, int64_t t0, uint32_t dst, int lane) {
-    const int64_t base = (u.b * a.Hkv + u.kvh) * a.Nk;
+  static constexpr bool kBulk = false;
+  __device__ __forceinline__ void look(const DecodeArgs&, const Unit&, int, int) {}
+  __device__ __forceinline__ void fetch(const DecodeArgs& a, const Unit& u, int t0, uint32_t dst, uint32_t, int lane) {
+    const int64_t base = ((int64_t)u.b * a.Hkv + u.kvh) * a.Nk;
 #pragma unroll
     for (int i = 0; i < TOK * CH / 32; ++i) {
       const int e = i * 32 + lane, t = e / CH, c = e % CH;
-      const int64_t key = t0 + t;
+      const int key = t0 + t;
       // keys that no row of the unit sees are not read: they come as zeros
       const bool live = key < u.n_k && (key >= u.lo || key < u.n_sink);
       const int64_t at = (base + (live ? key : 0)) * D + c * 8;
@@ -369,14 +389,14 @@ struct Bf16 {
 };
 
 // Row R of the sequence's n_q * group rows on kv head kvh: its token and query head.
-__device__ __forceinline__ int64_t row_off(const DecodeArgs& a, const Unit& u, int64_t R, int64_t sb, int64_t st, int64_t sh) {
-  const int64_t i = R / a.group, h = (int64_t)u.kvh * a.group + R % a.group;
+__device__ __forceinline__ int64_t row_off(const DecodeArgs& a, const Unit& u, int R, int64_t sb, int64_t st, int64_t sh) {
+  const int i = R / a.group, h = u.kvh * a.group + R % a.group;
   return (a.cu_q ? (u.q0 + i) * st : u.b * sb + i * st) + h * sh;
 }
 
 // o (unnormalised, relative to m) of 8 channels of row R, to its place.
 template <int D>
-__device__ __forceinline__ void finish_row(const DecodeArgs& a, const Unit& u, int64_t R, int c8, float m, float l, const float* o) {
+__device__ __forceinline__ void finish_row(const DecodeArgs& a, const Unit& u, int R, int c8, float m, float l, const float* o) {
   const int64_t off = row_off(a, u, R, a.o_sb, a.o_st, a.o_sh);
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // no visible key: zeros; NaN stays
   uint4 w;
@@ -392,20 +412,26 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
   constexpr int ROWS = 8 * NQ, TOK = F::TOK;
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ int64_t scan[kWarps];
-  __shared__ int64_t found_b, found_off;
+  __shared__ int64_t found_off;
+  __shared__ int found_b;
   __shared__ float wm[kWarps][ROWS], wl[kWarps][ROWS];
+  __shared__ __align__(8) uint64_t bars[kWarps][F::STAGES];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, t4 = lane & 3;
+  if (F::kBulk && tid < kWarps * F::STAGES) {
+    bar_init(smem_addr(&bars[0][0] + tid), F::SUBS);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
 
   // Where this piece of the line of tiles starts.
-  const int64_t per_thread = (a.B + kThreads - 1) / kThreads;
-  const int64_t b0 = min64(a.B, tid * per_thread), b1 = min64(a.B, b0 + per_thread);
+  const int per_thread = (a.B + kThreads - 1) / kThreads;
+  const int b0 = min(a.B, tid * per_thread), b1 = min(a.B, b0 + per_thread);
   int64_t sum = 0;
-  for (int64_t b = b0; b < b1; ++b) {
+  for (int b = b0; b < b1; ++b) {
     Unit u;
-    int64_t rt, tl;
+    int rt, tl;
     sequence<TOK, ROWS>(a, b, u, rt, tl);
-    sum += rt * a.Hkv * tl;
+    sum += (int64_t)rt * a.Hkv * tl;
   }
   int64_t inc = sum;
   for (int o = 1; o < 32; o <<= 1) {
@@ -413,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
     if (lane >= o) inc += x;
   }
   if (lane == 31) scan[warp] = inc;
-  if (tid == 0) found_b = -1;
+  if (tid == 0) found_b = a.B;
   __syncthreads();
   int64_t before = 0, W = 0;
   for (int w = 0; w < kWarps; ++w) {
@@ -424,11 +450,11 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
   const int64_t start = min64(W, blockIdx.x * per), end = min64(W, start + per);
   int64_t pos = before + inc - sum;
   if (start < end && start >= pos && start < pos + sum) {
-    for (int64_t b = b0; b < b1; ++b) {
+    for (int b = b0; b < b1; ++b) {
       Unit u;
-      int64_t rt, tl;
+      int rt, tl;
       sequence<TOK, ROWS>(a, b, u, rt, tl);
-      const int64_t n = rt * a.Hkv * tl;
+      const int64_t n = (int64_t)rt * a.Hkv * tl;
       if (start < pos + n) {
         found_b = b;
         found_off = start - pos;
@@ -439,42 +465,62 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
   }
   __syncthreads();
   Piece piece{};
-  int64_t b = found_b, off = found_off;
+  int b = found_b;
+  int64_t off = found_off;
 
   F f;
   const uint32_t ring = smem_addr(sm) + warp * (F::STAGES * F::STAGE);
   const uint8_t* ring_p = sm + warp * (F::STAGES * F::STAGE);
+  const uint32_t bar = smem_addr(&bars[warp][0]);
+  int in = 0, out = 0;        // the stages that are filled and read next
+  uint32_t phase = 0;         // of the stage that is read next
   int64_t at = start;
   while (at < end && b < a.B) {
     Unit u;
-    int64_t rt, tl;
+    int rt, tl;
     sequence<TOK, ROWS>(a, b, u, rt, tl);
-    const int64_t whole = rt * a.Hkv * tl;
+    const int64_t whole = (int64_t)rt * a.Hkv * tl;
     if (off >= whole) {   // next sequence
       off -= whole;
       ++b;
       continue;
     }
-    const int64_t unit = off / tl, i0 = off - unit * tl;
-    u.kvh = (int32_t)(unit % a.Hkv);
-    u.row0 = (int32_t)(unit / a.Hkv) * ROWS;
-    const int64_t i1 = min64(tl, i0 + (end - at));
-    const int64_t rows_all = u.n_q * a.group;
+    const int unit = (int)(off / tl), i0 = (int)(off - (int64_t)unit * tl);
+    u.kvh = unit % a.Hkv;
+    u.row0 = (unit / a.Hkv) * ROWS;
+    const int i1 = (int)min64(tl, i0 + (end - at));
+    const int rows_all = u.n_q * a.group;
+
+    const int first = i0 + warp;
+    const int mine = first < i1 ? (i1 - first + kWarps - 1) / kWarps : 0;
+    int sent = 0;
+    if (mine > 0) f.look(a, u, tile_at(u, first) * TOK, lane);
+    auto send = [&]() {
+      if (sent < mine) {
+        f.fetch(a, u, tile_at(u, first + sent * kWarps) * TOK, ring + in * F::STAGE, bar + in * 8, lane);
+        in = in + 1 == F::STAGES ? 0 : in + 1;
+        ++sent;
+        if (sent < mine) f.look(a, u, tile_at(u, first + sent * kWarps) * TOK, lane);
+      }
+      if (!F::kBulk) cp_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < F::STAGES - 1; ++s) send();
 
     uint32_t q[NQ][F::QREGS];
-    int64_t qpos[NQ][2];   // positions of this lane's columns (query rows)
+    int qpos[NQ][2];   // positions of this lane's columns (query rows)
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      const int64_t R = u.row0 + 8 * n + r;
+      const int R = u.row0 + 8 * n + r;
       const bool live = R < rows_all;
       F::load_q(a.q + row_off(a, u, live ? R : 0, a.q_sb, a.q_st, a.q_sh), live, t4, q[n]);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) qpos[n][c] = u.n_k - u.n_q + min64(rows_all - 1, u.row0 + 8 * n + 2 * t4 + c) / a.group;
+      for (int c = 0; c < 2; ++c) qpos[n][c] = u.n_k - u.n_q + min(rows_all - 1, u.row0 + 8 * n + 2 * t4 + c) / a.group;
     }
-    const int64_t p_min = u.n_k - u.n_q + u.row0 / a.group;
-    const int64_t p_max = u.n_k - u.n_q + min64(rows_all - 1, u.row0 + ROWS - 1) / a.group;
+    const int p_min = u.n_k - u.n_q + u.row0 / a.group;
+    const int p_max = u.n_k - u.n_q + min(rows_all - 1, u.row0 + ROWS - 1) / a.group;
 
-    float o[NQ][F::TILES][4], m[NQ][2], l[NQ][2];
+    float o[NQ][F::TILES][4], m[NQ][2], l[NQ][2];   // m: log2 units
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
 #pragma unroll
@@ -485,26 +531,19 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
       l[n][0] = l[n][1] = 0.f;
     }
 
-    const int64_t first = i0 + warp;
-    const int64_t mine = first < i1 ? (i1 - first + kWarps - 1) / kWarps : 0;
-    if (mine > 0) f.look(a, u, tile_at<TOK>(u, first) * TOK);
-    int64_t sent = 0;
-    auto send = [&]() {
-      if (sent < mine) {
-        f.fetch(a, u, tile_at<TOK>(u, first + sent * kWarps) * TOK, ring + (uint32_t)(sent % F::STAGES) * F::STAGE, lane);
-        ++sent;
-        if (sent < mine) f.look(a, u, tile_at<TOK>(u, first + sent * kWarps) * TOK);
-      }
-      cp_commit();
-    };
-#pragma unroll
-    for (int s = 0; s < F::STAGES - 1; ++s) send();
-    for (int64_t i = 0; i < mine; ++i) {
-      cp_wait<F::STAGES - 2>();
+    for (int i = 0; i < mine; ++i) {
+      if (F::kBulk)
+        bar_wait(bar + out * 8, phase, a.status);
+      else
+        cp_wait<F::STAGES - 2>();
       __syncwarp();
+      const uint8_t* st = ring_p + out * F::STAGE;
       send();
-      const uint8_t* st = ring_p + (i % F::STAGES) * F::STAGE;
-      const int64_t t0 = tile_at<TOK>(u, first + i * kWarps) * TOK;
+      if (++out == F::STAGES) {
+        out = 0;
+        phase ^= 1;
+      }
+      const int t0 = tile_at(u, first + i * kWarps) * TOK;
       float s[F::SUBS][NQ][4];
 #pragma unroll
       for (int x = 0; x < F::SUBS; ++x) F::template scores<NQ>(st, x, q, lane, s[x]);
@@ -513,12 +552,6 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
       uint32_t keep[F::SUBS];
 #pragma unroll
       for (int x = 0; x < F::SUBS; ++x) keep[x] = 0xFFFFu;
-#pragma unroll
-      for (int x = 0; x < F::SUBS; ++x)
-#pragma unroll
-        for (int n = 0; n < NQ; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[x][n][e] *= a.scale_log2;
       if (!all) {
 #pragma unroll
         for (int x = 0; x < F::SUBS; ++x) {
@@ -526,12 +559,12 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
           for (int n = 0; n < NQ; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int64_t key = t0 + 16 * x + r + 8 * (e >> 1), p = qpos[n][e & 1];
+              const int key = t0 + 16 * x + r + 8 * (e >> 1), p = qpos[n][e & 1];
               const bool see = key < u.n_k && key <= p && (a.window == 0 || p - key < a.window || key < a.sinks);
               if (!see) s[x][n][e] = -INFINITY;
             }
           // tokens that some row of the unit may see
-          const int64_t k0 = t0 + 16 * x + (lane & 15);
+          const int k0 = t0 + 16 * x + (lane & 15);
           keep[x] = __ballot_sync(0xffffffffu, k0 < u.n_k && (k0 >= u.lo || k0 < u.n_sink)) & 0xFFFFu;
         }
       }
@@ -546,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
           for (int y = 1; y < F::SUBS; ++y) x = fmaxf(x, fmaxf(s[y][n][c], s[y][n][c + 2]));
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-          const float mn = fmaxf(m[n][c], x);
+          const float mn = fmaxf(m[n][c], x * a.scale_log2);   // the scale is positive
           ref[n][c] = mn == -INFINITY ? 0.f : mn;
           corr[n][c] = ex2f(m[n][c] - ref[n][c]);
           moved |= mn != m[n][c];
@@ -573,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
         for (int n = 0; n < NQ; ++n) {
           float e[4];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) e[y] = ex2f(s[x][n][y] - ref[n][y & 1]);
+          for (int y = 0; y < 4; ++y) e[y] = ex2f(fmaf(s[x][n][y], a.scale_log2, -ref[n][y & 1]));
           l[n][0] += e[0] + e[2];
           l[n][1] += e[1] + e[3];
           p[n][0] = transpose8(pack2bf(e[0], e[1]));
@@ -582,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
         F::template accumulate<NQ>(st, x, p, keep[x], lane, o);
       }
     }
-    cp_wait<0>();
+    if (!F::kBulk) cp_wait<0>();
 
     // Join the four warps' parts in shared memory (over the rings).
 #pragma unroll
@@ -624,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
 #pragma unroll
         for (int x = 0; x < 8; ++x) acc[x] += g * src[x];
       }
-      const int64_t R = u.row0 + row;
+      const int R = u.row0 + row;
       if (R >= rows_all) continue;
       if (begins && ends) {
         finish_row<D>(a, u, R, c8, mx, ls, acc);
@@ -635,66 +668,95 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
         if (c8 == 0) *reinterpret_cast<float2*>(a.part_ml + (slot * ROWS + row) * 2) = make_float2(mx, ls);
       }
     }
-    if (!begins) {
-      piece.has_head = 1;
-      piece.head_ends = ends;
-    } else if (!ends) {
-      piece.has_tail = 1;
-      piece.b = (int32_t)u.b;
+    if (begins && !ends) {
+      piece.last = blockIdx.x + (int)((tl - i1 + per - 1) / per);   // every piece but the last one holds `per` tiles
+      piece.b = u.b;
       piece.row0 = u.row0;
       piece.kvh = u.kvh;
     }
     at += i1 - i0;
     off += i1 - i0;
+    // The rings are filled next by the async proxy, after these generic accesses.
+    if (F::kBulk) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
   }
   if (tid == 0) a.pieces[blockIdx.x] = piece;
 }
 
 // Adds up the parts of the unit that begins in piece blockIdx.x and ends in a
-// later one, in the order of the pieces.  Launched as a dependent of
-// decode_kernel: it waits for that grid's writes.
+// later one.  The parts are dealt to groups of threads, one thread 8 channels
+// of a row, and the groups' sums joined in order: a long sequence alone has some
+// 40 parts a unit, and one thread after another would wait for each.  Launched
+// as a dependent of decode_kernel: it waits for that grid's writes.
 template <class F, int D, int NQ>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ DecodeArgs a, int pieces) {
-  constexpr int ROWS = 8 * NQ;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ DecodeArgs a) {
+  constexpr int ROWS = 8 * NQ, C8 = D / 8, BATCH = 4;
+  __shared__ float part[kJoinThreads][11];   // m, l and 8 sums of a thread
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Piece p = a.pieces[blockIdx.x];
-  if (!p.has_tail) return;
-  int last = blockIdx.x;   // the piece that ends the unit
-  while (last + 1 < pieces) {
-    ++last;
-    if (a.pieces[last].head_ends) break;
-  }
+  if (p.last == 0) return;
   Unit u;
-  int64_t rt, tl;
+  int rt, tl;
   sequence<F::TOK, ROWS>(a, p.b, u, rt, tl);
   u.row0 = p.row0;
   u.kvh = p.kvh;
-  const int64_t rows_all = u.n_q * a.group;
-  for (int e = threadIdx.x; e < ROWS * (D / 8); e += kJoinThreads) {
-    const int row = e / (D / 8), c8 = e % (D / 8);
-    if (u.row0 + row >= rows_all) continue;
-    float m = -INFINITY, l = 0.f, acc[8] = {};
-    for (int w = blockIdx.x; w <= last; ++w) {
-      const int64_t slot = (int64_t)w * 2 + (w == (int)blockIdx.x ? 1 : 0);
-      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (slot * ROWS + row) * 2);
-      const float* src = a.part_o + (slot * ROWS + row) * D + c8 * 8;
-      const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + 4);
-      const float mn = fmaxf(m, ml.x), rf = mn == -INFINITY ? 0.f : mn;
-      const float g = ex2f(m - rf), h = ex2f(ml.x - rf);
-      l = l * g + ml.y * h;
-      const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  const int rows = min(ROWS, u.n_q * a.group - u.row0), items = rows * C8;
+  const int groups = kJoinThreads / items, item = threadIdx.x % items, g = threadIdx.x / items;
+  const int row = item / C8, c8 = item % C8;
+  float m = -INFINITY, l = 0.f, acc[8] = {};
+  auto add = [&](float pm, float pl, const float* v) {
+    const float mn = fmaxf(m, pm), rf = mn == -INFINITY ? 0.f : mn;
+    const float x = ex2f(m - rf), y = ex2f(pm - rf);
+    l = l * x + pl * y;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = acc[i] * g + v[i] * h;
-      m = mn;
+    for (int i = 0; i < 8; ++i) acc[i] = acc[i] * x + v[i] * y;
+    m = mn;
+  };
+  if (g < groups) {
+    for (int w0 = blockIdx.x + g; w0 <= p.last; w0 += BATCH * groups) {
+      float2 ml[BATCH];
+      float v[BATCH][8];
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) {
+        const int w = w0 + i * groups;
+        ml[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
+        if (w <= p.last) {
+          const int64_t at = ((int64_t)w * 2 + (w == (int)blockIdx.x ? 1 : 0)) * ROWS + row;
+          ml[i] = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+          *reinterpret_cast<float4*>(v[i]) = *reinterpret_cast<const float4*>(a.part_o + at * D + c8 * 8);
+          *reinterpret_cast<float4*>(v[i] + 4) = *reinterpret_cast<const float4*>(a.part_o + at * D + c8 * 8 + 4);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < BATCH; ++i) add(ml[i].x, ml[i].y, v[i]);
     }
-    finish_row<D>(a, u, u.row0 + row, c8, m, l, acc);
+    float* d = part[threadIdx.x];
+    d[0] = m;
+    d[1] = l;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d[2 + i] = acc[i];
   }
+  __syncthreads();
+  if (g != 0) return;
+  for (int k = 1; k < groups; ++k) {
+    const float* d = part[k * items + item];
+    add(d[0], d[1], d + 2);
+  }
+  finish_row<D>(a, u, u.row0 + row, c8, m, l, acc);
 }
 
 size_t ws_bytes(int64_t rows, int64_t d) {
   return align_up(kWorkers * sizeof(Piece), 256) + align_up((size_t)kWorkers * 2 * rows * 2 * sizeof(float), 256) +
          (size_t)kWorkers * 2 * rows * d * sizeof(float);
+}
+
+// A window that reaches past every key is none; so no position minus window
+// leaves 31 bits.
+void set_window(DecodeArgs& a, int64_t window, int64_t sinks) {
+  a.window = window >= a.Nk ? 0 : (int32_t)window;
+  a.sinks = (int32_t)min64(sinks, a.Nk);
 }
 
 template <class F, int D, int NQ>
@@ -723,7 +785,7 @@ sa_status launch(DecodeArgs& a, int64_t max_tiles, void* ws, cudaStream_t st) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, join_kernel<F, D, NQ>, a, grid) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, join_kernel<F, D, NQ>, a) != cudaSuccess)
     return check_launch("join_kernel");
   return SA_OK;
 }
@@ -757,9 +819,8 @@ sa_status launch_kv4_attn(const Kv4AttnArgs& x, cudaStream_t st) {
   a.Nq = 1;
   a.Nk = x.max_blocks * x.desc.page;
   a.max_blocks = x.max_blocks;
-  a.num_pages = x.desc.num_pages;
-  a.window = x.window;
-  a.sinks = x.sinks;
+  a.num_pages = (int32_t)x.desc.num_pages;
+  set_window(a, x.window, x.sinks);
   a.B = (int32_t)x.B;
   a.Hkv = (int32_t)x.desc.Hkv;
   a.group = (int32_t)(x.Hq / x.desc.Hkv);
@@ -788,8 +849,7 @@ sa_status launch_window_decode(const WindowArgs& x, cudaStream_t st) {
   a.q_sb = a.o_sb = s.Hq * s.Nq * s.d;
   a.Nq = s.Nq;
   a.Nk = s.Nk;
-  a.window = x.window;
-  a.sinks = x.sinks;
+  set_window(a, x.window, x.sinks);
   a.B = (int32_t)s.B;
   a.Hkv = (int32_t)s.Hkv;
   a.group = (int32_t)(s.Hq / s.Hkv);

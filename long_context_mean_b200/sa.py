@@ -442,18 +442,18 @@ def _need(ok, msg):
 
 
 def _same(t, dtype, shape, name, device, contiguous=True):
-    """t is a CUDA tensor of this dtype, shape and device.  (The messages are
-    built only for a tensor that is refused: a step of single tokens makes
-    some thirty of these checks.)"""
-    import torch
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype):
-        raise ValueError(f"{name} must be a {dtype} tensor")
-    if t.device != device or device.type != "cuda":
-        raise ValueError(f"{name} must be on the same CUDA device as the other tensors")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    """t is a CUDA tensor of this dtype, shape and device."""
+    try:
+        if (t.dtype is dtype and t.device == device and t.is_cuda and t.shape == shape
+                and (not contiguous or t.is_contiguous())):
+            return
+    except AttributeError:
+        raise ValueError(f"{name} must be a {dtype} tensor") from None
+    # (the messages are built only here: a step of single tokens makes some thirty of these checks)
+    _need(t.dtype is dtype, f"{name} must be a {dtype} tensor")
+    _need(t.device == device and t.is_cuda, f"{name} must be on the same CUDA device as the other tensors")
+    _need(t.shape == shape, f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    _need(False, f"{name} must be contiguous")
 
 
 def _index(t, n, name, device):
@@ -472,13 +472,12 @@ def _at(t):
 def _on(device, stream, fn, *args):
     """fn(*args, stream) with `device` current."""
     import torch
-    if device.index == torch.cuda.current_device():
-        s = torch.cuda.current_stream() if stream is None else stream
-        code = fn(*args, s.cuda_stream)
+    if device.index == torch._C._cuda_getDevice():
+        # (the raw stream: torch.cuda.current_stream() takes 3 us, the rest of a call 8)
+        code = fn(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(device):
-            s = torch.cuda.current_stream() if stream is None else stream
-            code = fn(*args, s.cuda_stream)
+            code = fn(*args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream)
     if code != SA_OK:
         _check(code)
 
@@ -631,6 +630,7 @@ class Rope:
         self.magnitude = float(mag.value)
         self.host_freqs = host              # uint64 bits: turns per position in units of 2^-64
         self.freqs = host.to(device)
+        self.descs = {}                     # descriptions of the calls' sizes and strides
 
 
 def _rope_strides(t, name, shape, dtype, dev):
@@ -664,8 +664,13 @@ def rope(rope: Rope, pos, q, q_out, k=None, k_out=None, *, inverse=False, stream
     _same(pos, torch.int32, lead if batched else (N,), "pos", dev, contiguous=False)
     _need(N <= 1 or pos.stride(-1) == 1, "the positions of a sequence must be contiguous")
     _need(rope.freqs.device == dev, "the frequencies must be on the tensors' device")
-    desc = RopeDesc(B, N, shape[-2], Hk, d, qs, qo, ks, ko, pos.stride(0) if batched else 0, rope.rot_dim, rope.layout,
-                    dtype_code(q), int(bool(inverse)), rope.magnitude, 0)
+    key = (dt, B, N, shape[-2], Hk, d, qs, qo, ks, ko, pos.stride(0) if batched else 0, bool(inverse))
+    desc = rope.descs.get(key)
+    if desc is None:
+        desc = RopeDesc(*key[1:11], rope.rot_dim, rope.layout, dtype_code(q), int(bool(inverse)), rope.magnitude, 0)
+        if len(rope.descs) >= 64:
+            rope.descs.clear()
+        rope.descs[key] = desc
     _on(dev, stream, load().sa_rope, q.data_ptr(), q_out.data_ptr(), _at(k), _at(k_out), pos.data_ptr(),
         rope.freqs.data_ptr(), ctypes.byref(desc))
 
