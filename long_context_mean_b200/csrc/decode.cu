@@ -22,11 +22,17 @@
 //    group of 8 rows wastes nothing.  (tcgen05 wants its operands in shared
 //    memory: the widened codes would have to be written there, 4 times the bytes
 //    that arrive.)
-//  * KV4: codes become bf16 integers in registers (one AND-OR puts a nibble
-//    into the mantissa of 128.0, a subtraction of 136 leaves code - 8); K's scales
-//    multiply the 32-channel partial scores in fp32, V's scales multiply P.
+//  * KV4, bound by the instructions that widen the codes: a nibble under a mask is
+//    an fp16 (K) or bf16 (V) number already (below), five instructions for 8 codes,
+//    and products with constants take the offset 8 off; K's scales multiply the
+//    32-channel partial scores in fp32, V's scales multiply P.  16 sequences of 8,000
+//    to 30,000 tokens, 312 MB: 75 us (4.2 TB/s); nibbles widened to bf16 integers by
+//    shift, AND-OR and subtraction took 108, 8-bit operands (converted back to
+//    fp16 by the compiler) 165.
 // Rounding: P (and P times the V scale) is rounded to bf16 for the second
 // product; sums, maxima and outputs are fp32.
+#include <cuda_fp16.h>
+
 #include "sa_internal.cuh"
 
 namespace sa {
@@ -34,11 +40,14 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kWorkers = 592;      // 148 SMs * 4 CTAs
+constexpr int kWorkers = 444;      // 148 SMs * 3 CTAs
 constexpr int kMinTiles = 4;       // tiles a piece holds at least: one per warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kJoinThreads = 256;
+// The reference maximum moves (and O with it) only when a score passes it by
+// 2^8: with every new maximum a fifth of the tiles would rescale 64 numbers.
+constexpr float kRescale = 8.f;
 
 // What a worker leaves for join_kernel.
 struct Piece {
@@ -65,7 +74,7 @@ struct DecodeArgs {
   int64_t o_sb, o_st, o_sh;      // of out (lse: the same / d)
   int64_t T, Nq, Nk;             // packed tokens; tokens and keys per sequence at most
   int64_t max_blocks;
-  int32_t num_pages, window, sinks;
+  int32_t num_pages, page_bytes, window, sinks;
   int32_t B, Hkv, group, lg_page;
   float scale_log2;
 };
@@ -123,6 +132,19 @@ __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uin
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16816z(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {   // d = a b
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+// The same on fp16 operands, d = a b + c.
+__device__ __forceinline__ void mma16816h(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1, float c0, float c1, float c2, float c3) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -132,18 +154,14 @@ __device__ __forceinline__ uint32_t pack2bf(float lo, float hi) {
   __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
 }
+__device__ __forceinline__ uint32_t pack2h(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
 __device__ __forceinline__ uint32_t mul2bf(uint32_t a, uint32_t b) {
   __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
   return *reinterpret_cast<uint32_t*>(&r);
 }
-// Nibbles I and I + 4 of w as a bf16 pair of code - 8 (exact).
-template <int I>
-__device__ __forceinline__ uint32_t codes2(uint32_t w) {
-  uint32_t x = ((w >> (4 * I)) & 0x000F000Fu) | 0x43004300u;   // 128 + code
-  __nv_bfloat162 h = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&x), __floats2bfloat162_rn(136.f, 136.f));
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-
 // One unit: a sequence's row tile on one kv head, and the tiles it visits.
 // (Tokens and keys of a sequence fit 30 bits.)
 struct Unit {
@@ -194,21 +212,69 @@ __device__ __forceinline__ int tile_at(const Unit& u, int i) { return i < u.sink
 // as B operands.
 template <int D>
 struct Kv4 {
-  static constexpr int G = D / 32, SUBS = 2, TOK = 16 * SUBS, SUB_BYTES = 576 * G, STAGE = SUBS * SUB_BYTES;
-  static constexpr int STAGES = 3, QREGS = 4 * G, TILES = D / 16;
-  static constexpr int CTAS = 4;
+  static constexpr int G = D / 32, SUBS = 4, TOK = 16 * SUBS, SUB_BYTES = 576 * G, STAGE = SUBS * SUB_BYTES;
+  // 64 tokens a tile, two stages a warp, 12 warps an SM: 75 us for 312 MB, with 32
+  // tokens and three stages 83 (12 warps) and 87 (16, whose 128 registers spill).
+  static constexpr int STAGES = 2, TILES = D / 16;
+  static constexpr int CTAS = 3;
   // Channel of accumulator tile j's row lane / 4 (+ 8 where half).
   static __device__ __forceinline__ int channel(int j, int half, int r) { return 32 * (j >> 1) + 4 * r + 2 * (j & 1) + half; }
-  static __device__ __forceinline__ void load_q(const uint16_t* p, bool live, int q4, uint32_t* q) {
+  // A row of q in fp16: its values times 2^x, with 2^x chosen so that the
+  // largest lies in [2^14, 2^15): bf16's 8 bits fit fp16's 11, exact down to
+  // 2^-31 of the largest.  `off` holds - 8 2^-24 times the groups' sums in three
+  // bf16 parts each, as the columns of one product with the tokens' scales
+  // (k = group, + 4 the second part, + 8 the third); `unit` is the factor
+  // scale log2(e) 2^(24 - x) of this lane's scores.
+  struct Q {
+    uint32_t part[4 * G], off[2];
+    float unit[2];
+  };
+  static __device__ __forceinline__ void load_q(const uint16_t* p, bool live, int lane, float scale_log2, Q& q) {
+    const int q4 = lane & 3;
+    uint4 w[G];
+    uint32_t top = 0;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (live) w = *reinterpret_cast<const uint4*>(p + 32 * g + 8 * q4);
-      q[4 * g + 0] = __byte_perm(w.x, w.z, 0x5410);   // channels 0 and 4 of the lane's 8
-      q[4 * g + 1] = __byte_perm(w.x, w.z, 0x7632);
-      q[4 * g + 2] = __byte_perm(w.y, w.w, 0x5410);
-      q[4 * g + 3] = __byte_perm(w.y, w.w, 0x7632);
+      w[g] = make_uint4(0, 0, 0, 0);
+      if (live) w[g] = *reinterpret_cast<const uint4*>(p + 32 * g + 8 * q4);
+      const uint32_t x[4] = {w[g].x, w[g].y, w[g].z, w[g].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = max(top, max(x[e] & 0x7FFFu, (x[e] >> 16) & 0x7FFFu));
     }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int x = min(127, 141 - (int)(top >> 7));
+    const float up = __uint_as_float((uint32_t)(127 + x) << 23);
+    const float unit = scale_log2 * 0x1p24f / up;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) q.unit[c] = __shfl_sync(0xffffffffu, unit, (2 * q4 + c) * 4);
+    float lead[2] = {0.f, 0.f};   // the sums of groups 2 (q4 % 2), + 1
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      float f[8];
+      unpack16(w[g], uint16_t{}, f);
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        f[e] *= up;
+        sum += f[e];
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      if (g >> 1 == (q4 & 1)) lead[g & 1] = sum * -0x1p-21f;
+      // pairs (e, e + 4); the odd ones meet codes at 16 times their value
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q.part[4 * g + e] = pack2h(f[e] * (e & 1 ? 0.0625f : 1.f), f[e + 4] * (e & 1 ? 0.0625f : 1.f));
+    }
+    uint32_t b[3];
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+      b[n] = pack2bf(lead[0], lead[1]);
+      lead[0] -= __uint_as_float(b[n] << 16);
+      lead[1] -= __uint_as_float(b[n] & 0xFFFF0000u);
+    }
+    q.off[0] = q4 < 2 ? b[0] : b[1];
+    q.off[1] = q4 < 2 ? b[2] : 0u;
   }
   // Lane s < SUBS looks up and fetches subtile s: one bulk copy of its bytes,
   // which the stage's mbarrier counts.  A subtile that no row sees is left
@@ -216,49 +282,63 @@ struct Kv4 {
   // replaced by zero.
   static constexpr bool kBulk = true;
   static constexpr int32_t kSkip = INT32_MIN;
-  int32_t page = kSkip;   // table entry of the tile that is fetched next
-  __device__ __forceinline__ void look(const DecodeArgs& a, const Unit& u, int t0, int lane) {
-    const int at = t0 + 16 * lane;
-    const bool seen = lane < SUBS && at < u.n_k && (at + 16 > u.lo || at < u.n_sink);
-    page = seen ? max(-1, a.table[(int64_t)u.b * a.max_blocks + (at >> a.lg_page)]) : kSkip;
+  // The unit's place in the tables and the cache, in subtiles of 16 tokens.
+  const int32_t* row;
+  const uint8_t* base;
+  int32_t lo, n_sink, n;
+  int32_t page = kSkip, sub = 0;   // table entry and number of this lane's subtile that is fetched next
+  __device__ __forceinline__ void start(const DecodeArgs& a, const Unit& u, int lane) {
+    row = a.table + (int64_t)u.b * a.max_blocks;
+    base = a.cache + ((int64_t)u.kvh << (a.lg_page - 4)) * SUB_BYTES;
+    lo = u.lo >> 4;
+    n_sink = (u.n_sink + 15) >> 4;
+    n = lane < SUBS ? (u.n_k + 15) >> 4 : 0;
   }
-  __device__ __forceinline__ void fetch(const DecodeArgs& a, const Unit& u, int t0, uint32_t dst, uint32_t bar, int lane) {
+  __device__ __forceinline__ void look(const DecodeArgs& a, int tile, int lane) {
+    sub = tile * SUBS + lane;
+    page = kSkip;
+    if (sub < n && (sub >= lo || sub < n_sink)) page = max(-1, row[sub >> (a.lg_page - 4)]);
+  }
+  __device__ __forceinline__ void fetch(const DecodeArgs& a, const Unit&, int, uint32_t dst, uint32_t bar, int lane) {
     if (lane >= SUBS) return;
     const bool seen = page != kSkip;
     bar_expect(bar, seen ? SUB_BYTES : 0);
     if (!seen) return;
     int pg = page;
-    if (pg < 0 || pg >= a.num_pages) {   // the sequence's result is not defined, the access stays inside
+    if ((uint32_t)pg >= (uint32_t)a.num_pages) {   // the sequence's result is not defined, the access stays inside
       raise_status(a.status, SA_ERR_INVALID_ARG);
       pg = 0;
     }
-    const int in = ((t0 + 16 * lane) & ((1 << a.lg_page) - 1)) >> 4;
-    bulk_load(dst + lane * SUB_BYTES, a.cache + ((((int64_t)pg * a.Hkv + u.kvh) << (a.lg_page - 4)) + in) * SUB_BYTES,
-              SUB_BYTES, bar);
+    const int in = sub & ((1 << (a.lg_page - 4)) - 1);
+    bulk_load(dst + lane * SUB_BYTES, base + (int64_t)pg * a.page_bytes + in * SUB_BYTES, SUB_BYTES, bar);
   }
+  // A code + 8 in the low bits of a half word is the fp16 subnormal
+  // (code + 8) 2^-24, and one nibble higher 16 times that: K's operands take a mask
+  // each and a shift for two, and the offset 8 goes into the accumulator.
   template <int NQ>
-  static __device__ __forceinline__ void scores(const uint8_t* st, int s, const uint32_t (*q)[QREGS], int lane, float (*out)[4]) {
+  static __device__ __forceinline__ void scores(const uint8_t* st, int s, const Q* q, int lane, float (*out)[4]) {
     const uint8_t* p = st + s * SUB_BYTES;
     uint32_t w0[G], w1[G];
     ld<G>(p + lane * 4 * G, w0);
     ld<G>(p + 128 * G + lane * 4 * G, w1);
-    uint16_t s0[G], s1[G];
-    ld<G / 2>(p + 512 * G + (lane >> 2) * 2 * G, reinterpret_cast<uint32_t*>(s0));
-    ld<G / 2>(p + 512 * G + ((lane >> 2) + 8) * 2 * G, reinterpret_cast<uint32_t*>(s1));
+    uint32_t s0[G / 2], s1[G / 2];
+    ld<G / 2>(p + 512 * G + (lane >> 2) * 2 * G, s0);
+    ld<G / 2>(p + 512 * G + ((lane >> 2) + 8) * 2 * G, s1);
+    // (G = 2: the columns of groups 2 and 3 are zero)
+    const uint32_t t0 = lane & 1 ? s0[G / 2 - 1] : s0[0], t1 = lane & 1 ? s1[G / 2 - 1] : s1[0];
 #pragma unroll
-    for (int n = 0; n < NQ; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) out[n][e] = 0.f;
+    for (int n = 0; n < NQ; ++n) mma16816z(out[n], t0, t1, t0, t1, q[n].off[0], q[n].off[1]);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const uint32_t a0 = codes2<0>(w0[g]), a1 = codes2<0>(w1[g]), a2 = codes2<1>(w0[g]), a3 = codes2<1>(w1[g]);
-      const uint32_t c0 = codes2<2>(w0[g]), c1 = codes2<2>(w1[g]), c2 = codes2<3>(w0[g]), c3 = codes2<3>(w1[g]);
-      const float f0 = bf16_to_f32(s0[g]), f1 = bf16_to_f32(s1[g]);
+      constexpr uint32_t L = 0x000F000Fu, H = 0x00F000F0u;
+      const uint32_t y0 = w0[g] >> 8, y1 = w1[g] >> 8;
+      const float f0 = __uint_as_float(g & 1 ? s0[g >> 1] & 0xFFFF0000u : s0[g >> 1] << 16);
+      const float f1 = __uint_as_float(g & 1 ? s1[g >> 1] & 0xFFFF0000u : s1[g >> 1] << 16);
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
-        mma16816(c, a0, a1, a2, a3, q[n][4 * g], q[n][4 * g + 1]);
-        mma16816(c, c0, c1, c2, c3, q[n][4 * g + 2], q[n][4 * g + 3]);
+        float c[4];
+        mma16816h(c, w0[g] & L, w1[g] & L, w0[g] & H, w1[g] & H, q[n].part[4 * g], q[n].part[4 * g + 1], 0.f, 0.f, 0.f, 0.f);
+        mma16816h(c, y0 & L, y1 & L, y0 & H, y1 & H, q[n].part[4 * g + 2], q[n].part[4 * g + 3], c[0], c[1], c[2], c[3]);
         out[n][0] = fmaf(c[0], f0, out[n][0]);
         out[n][1] = fmaf(c[1], f0, out[n][1]);
         out[n][2] = fmaf(c[2], f1, out[n][2]);
@@ -266,6 +346,13 @@ struct Kv4 {
       }
     }
   }
+  // A code + 8 in the low bits of a bf16 is (code + 8) 2^-133, one nibble
+  // higher 16 times that (bf16's subnormals and first binade are linear): masks
+  // again, and a product with a constant - 8 takes the offset off at once, so that
+  // the sums stay as small as without it.  P comes times 2^kShift, which keeps
+  // the products far from fp32's smallest numbers.
+  static constexpr float kShift = 64.f;
+  static __device__ __forceinline__ float gain(int half) { return half ? 0x1p65f : 0x1p69f; }   // 2^(133 - kShift), / 16
   // p: P as B operands (tokens 2 (lane % 4), + 1 and + 8, + 9).  keep: one bit per
   // token of the subtile whose V counts; a scale of any other token is
   // whatever the slot holds (possibly NaN) and is replaced by 0.
@@ -289,13 +376,15 @@ struct Kv4 {
     }
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const uint32_t a0 = codes2<0>(v0[g]), a1 = codes2<1>(v0[g]), a2 = codes2<0>(v1[g]), a3 = codes2<1>(v1[g]);
-      const uint32_t c0 = codes2<2>(v0[g]), c1 = codes2<3>(v0[g]), c2 = codes2<2>(v1[g]), c3 = codes2<3>(v1[g]);
+      constexpr uint32_t L = 0x000F000Fu, H = 0x00F000F0u, OFF = 0x80088008u, OFF16 = 0x80808080u;
+      const uint32_t y0 = v0[g] >> 8, y1 = v1[g] >> 8;
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         const uint32_t p0 = mul2bf(p[n][0], s0[g]), p1 = mul2bf(p[n][1], s1[g]);
-        mma16816(o[n][2 * g], a0, a1, a2, a3, p0, p1);
-        mma16816(o[n][2 * g + 1], c0, c1, c2, c3, p0, p1);
+        mma16816(o[n][2 * g], v0[g] & L, v0[g] & H, v1[g] & L, v1[g] & H, p0, p1);
+        mma16816(o[n][2 * g + 1], y0 & L, y0 & H, y1 & L, y1 & H, p0, p1);
+        mma16816(o[n][2 * g], OFF, OFF16, OFF, OFF16, p0, p1);
+        mma16816(o[n][2 * g + 1], OFF, OFF16, OFF, OFF16, p0, p1);
       }
     }
   }
@@ -313,23 +402,32 @@ struct Kv4 {
 template <int D>
 struct Bf16 {
   static constexpr int SUBS = 1, TOK = 16, STAGE = TOK * D * 4, STAGES = 3;
-  static constexpr int QREGS = D / 8, TILES = D / 16, CH = D / 8;   // chunks of a row
+  static constexpr int TILES = D / 16, CH = D / 8;   // CH: chunks of a row
+  static constexpr float kShift = 0.f;
+  static __device__ __forceinline__ float gain(int) { return 1.f; }
   static constexpr int CTAS = 2;
   static __device__ __forceinline__ int channel(int j, int half, int r) { return D == 128 ? 64 * half + 8 * r + j : 8 * r + 4 * half + j; }
-  static __device__ __forceinline__ void load_q(const uint16_t* p, bool live, int q4, uint32_t* q) {
+  struct Q {
+    uint32_t part[D / 8];
+    float unit[2];
+  };
+  static __device__ __forceinline__ void load_q(const uint16_t* p, bool live, int lane, float scale_log2, Q& q) {
 #pragma unroll
     for (int c = 0; c < CH / 4; ++c) {
       uint4 w = make_uint4(0, 0, 0, 0);
-      if (live) w = *reinterpret_cast<const uint4*>(p + (4 * c + q4) * 8);
-      q[4 * c] = w.x;
-      q[4 * c + 1] = w.y;
-      q[4 * c + 2] = w.z;
-      q[4 * c + 3] = w.w;
+      if (live) w = *reinterpret_cast<const uint4*>(p + (4 * c + (lane & 3)) * 8);
+      q.part[4 * c] = w.x;
+      q.part[4 * c + 1] = w.y;
+      q.part[4 * c + 2] = w.z;
+      q.part[4 * c + 3] = w.w;
     }
+    q.unit[0] = q.unit[1] = scale_log2;
   }
   static constexpr bool kBulk = false;
-  __device__ __forceinline__ void look(const DecodeArgs&, const Unit&, int, int) {}
-  __device__ __forceinline__ void fetch(const DecodeArgs& a, const Unit& u, int t0, uint32_t dst, uint32_t, int lane) {
+  __device__ __forceinline__ void start(const DecodeArgs&, const Unit&, int) {}
+  __device__ __forceinline__ void look(const DecodeArgs&, int, int) {}
+  __device__ __forceinline__ void fetch(const DecodeArgs& a, const Unit& u, int tile, uint32_t dst, uint32_t, int lane) {
+    const int t0 = tile * TOK;
     const int64_t base = ((int64_t)u.b * a.Hkv + u.kvh) * a.Nk;
 #pragma unroll
     for (int i = 0; i < TOK * CH / 32; ++i) {
@@ -343,7 +441,7 @@ struct Bf16 {
     }
   }
   template <int NQ>
-  static __device__ __forceinline__ void scores(const uint8_t* st, int, const uint32_t (*q)[QREGS], int lane, float (*out)[4]) {
+  static __device__ __forceinline__ void scores(const uint8_t* st, int, const Q* q, int lane, float (*out)[4]) {
     const int r = lane >> 2, q4 = lane & 3;
 #pragma unroll
     for (int n = 0; n < NQ; ++n)
@@ -356,8 +454,8 @@ struct Bf16 {
       const uint4 y = *reinterpret_cast<const uint4*>(st + (r + 8) * D * 2 + ch * 16);
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        mma16816(out[n], x.x, y.x, x.y, y.y, q[n][4 * c], q[n][4 * c + 1]);
-        mma16816(out[n], x.z, y.z, x.w, y.w, q[n][4 * c + 2], q[n][4 * c + 3]);
+        mma16816(out[n], x.x, y.x, x.y, y.y, q[n].part[4 * c], q[n].part[4 * c + 1]);
+        mma16816(out[n], x.z, y.z, x.w, y.w, q[n].part[4 * c + 2], q[n].part[4 * c + 3]);
       }
     }
   }
@@ -494,26 +592,29 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
     const int first = i0 + warp;
     const int mine = first < i1 ? (i1 - first + kWarps - 1) / kWarps : 0;
     int sent = 0;
-    if (mine > 0) f.look(a, u, tile_at(u, first) * TOK, lane);
+    f.start(a, u, lane);
+    int next = tile_at(u, first);   // the tile that is fetched next
+    if (mine > 0) f.look(a, next, lane);
     auto send = [&]() {
       if (sent < mine) {
-        f.fetch(a, u, tile_at(u, first + sent * kWarps) * TOK, ring + in * F::STAGE, bar + in * 8, lane);
+        f.fetch(a, u, next, ring + in * F::STAGE, bar + in * 8, lane);
         in = in + 1 == F::STAGES ? 0 : in + 1;
         ++sent;
-        if (sent < mine) f.look(a, u, tile_at(u, first + sent * kWarps) * TOK, lane);
+        next = tile_at(u, first + sent * kWarps);
+        if (sent < mine) f.look(a, next, lane);
       }
       if (!F::kBulk) cp_commit();
     };
 #pragma unroll
     for (int s = 0; s < F::STAGES - 1; ++s) send();
 
-    uint32_t q[NQ][F::QREGS];
+    typename F::Q q[NQ];
     int qpos[NQ][2];   // positions of this lane's columns (query rows)
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       const int R = u.row0 + 8 * n + r;
       const bool live = R < rows_all;
-      F::load_q(a.q + row_off(a, u, live ? R : 0, a.q_sb, a.q_st, a.q_sh), live, t4, q[n]);
+      F::load_q(a.q + row_off(a, u, live ? R : 0, a.q_sb, a.q_st, a.q_sh), live, lane, a.scale_log2, q[n]);
 #pragma unroll
       for (int c = 0; c < 2; ++c) qpos[n][c] = u.n_k - u.n_q + min(rows_all - 1, u.row0 + 8 * n + 2 * t4 + c) / a.group;
     }
@@ -579,7 +680,8 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
           for (int y = 1; y < F::SUBS; ++y) x = fmaxf(x, fmaxf(s[y][n][c], s[y][n][c + 2]));
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-          const float mn = fmaxf(m[n][c], x * a.scale_log2);   // the scale is positive
+          x *= q[n].unit[c];   // (positive)
+          const float mn = x > m[n][c] + kRescale ? x : m[n][c];   // m = -inf: any score is above
           ref[n][c] = mn == -INFINITY ? 0.f : mn;
           corr[n][c] = ex2f(m[n][c] - ref[n][c]);
           moved |= mn != m[n][c];
@@ -606,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
         for (int n = 0; n < NQ; ++n) {
           float e[4];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) e[y] = ex2f(fmaf(s[x][n][y], a.scale_log2, -ref[n][y & 1]));
+          for (int y = 0; y < 4; ++y) e[y] = ex2f(fmaf(s[x][n][y], q[n].unit[y & 1], F::kShift - ref[n][y & 1]));
           l[n][0] += e[0] + e[2];
           l[n][1] += e[1] + e[3];
           p[n][0] = transpose8(pack2bf(e[0], e[1]));
@@ -624,6 +726,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[n][c] += __shfl_xor_sync(0xffffffffu, l[n][c], d);
+        l[n][c] *= exp2f(-F::kShift);
         if (r == 0) {
           wm[warp][8 * n + 2 * t4 + c] = m[n][c];
           wl[warp][8 * n + 2 * t4 + c] = l[n][c];
@@ -638,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
       for (int j = 0; j < F::TILES; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          os[(warp * ROWS + 8 * n + 2 * t4 + (e & 1)) * OS + F::channel(j, e >> 1, r)] = o[n][j][e];
+          os[(warp * ROWS + 8 * n + 2 * t4 + (e & 1)) * OS + F::channel(j, e >> 1, r)] = o[n][j][e] * F::gain(e >> 1);
     __syncthreads();
     const bool begins = i0 == 0, ends = i1 == tl;
     const int64_t slot = (int64_t)blockIdx.x * 2 + (begins ? 1 : 0);
@@ -820,6 +923,7 @@ sa_status launch_kv4_attn(const Kv4AttnArgs& x, cudaStream_t st) {
   a.Nk = x.max_blocks * x.desc.page;
   a.max_blocks = x.max_blocks;
   a.num_pages = (int32_t)x.desc.num_pages;
+  a.page_bytes = (int32_t)(x.desc.Hkv * (x.desc.page / 16) * 18 * x.desc.d);
   set_window(a, x.window, x.sinks);
   a.B = (int32_t)x.B;
   a.Hkv = (int32_t)x.desc.Hkv;

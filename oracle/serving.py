@@ -16,21 +16,22 @@ def visible(n_q, n_k, window, sinks):
     return see & ((p - j < window) | (j < sinks)) if window else see
 
 
-def attention(q, k, v, window, sinks, scale=0.0):
+def attention(q, k, v, window, sinks, scale=0.0, extra=None):
     """One head: q [n_q, d], k, v [n_k, d].  Returns out, lse, and two sums for
-    error bounds: sum_j w_j |v_j| and the largest scale sum_c |q_c k_c| of a
-    visible key.  Keys that no row sees are left out."""
+    error bounds: sum_j w_j |v_j| and the largest scale sum_c |q_c| (|k_c| + extra_c)
+    of a visible key.  Keys that no row sees are left out."""
     q, k, v = (np.asarray(x, np.float64) for x in (q, k, v))
     n_q, d = q.shape
     scale = scale or 1 / math.sqrt(d)
     see = visible(n_q, k.shape[0], window, sinks)
     used = see.any(0)
     k, v, see = k[used], v[used], see[:, used]
+    big = np.abs(k) + (0 if extra is None else extra[used])
     out, absv = np.zeros((n_q, d)), np.zeros((n_q, d))
     lse, size = np.full(n_q, -np.inf), np.zeros(n_q)
     if used.any():
         s = np.where(see, q @ k.T * scale, -np.inf)
-        size = np.where(see, np.abs(q) @ np.abs(k).T * scale, 0).max(1)
+        size = np.where(see, np.abs(q) @ big.T * scale, 0).max(1)
         m = s.max(1)
         some = m > -np.inf
         e = np.exp(s - np.where(some, m, 0)[:, None])

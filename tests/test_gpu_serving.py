@@ -7,7 +7,12 @@ score is off by at most e = (d + 8) 2^-24 sum |q_c k_c| scale (fp32 products and
 sums, the scaling, the difference to the maximum; the power of two adds
 2^-22), so a weight is off by 2 e + 2^-21 relative (numerator and normaliser);
 bf16 weights (and for the 4-bit cache bf16 weight times scale) add u each, the
-output's rounding u |o|, and sums of n terms n 2^-24.
+output's rounding u |o|, and sums of n terms n 2^-24.  The cache's K enters as
+(code + 8) with 8 sum q taken off in the accumulator: every term and partial
+sum of a 32-channel group is then at most sum |q_c| (|code_c| + 8) times its scale,
+so e counts |k_c| + 8 s_c in the place of |k_c|, with 3 x 32 products, 32 terms of the
+sum of q, the offset, the scale and the 4 groups: below (d + 8) roundings of 2^-24 for
+d = 128 and below 140 for either d.
 """
 
 import math
@@ -280,7 +285,7 @@ def paged(torch, sa, c, seed=0):
         k, v = (torch.randn(n, Hkv, d, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
         slots = torch.tensor([order[used + i // page] * page + i % page for i in range(n)], dtype=torch.int32, device="cuda")
         sa.kv4_append(k, v, slots, cache)
-        vals.append([S.values(*S.quantise(f64(x))) for x in (k, v)])
+        vals.append([S.values(*S.quantise(f64(x))) for x in (k, v)] + [8 * np.repeat(S.quantise(f64(k))[1], 32, -1)])
         used += blocks[b]
     q = (torch.randn(sum(nq) + 2, Hq, d, device="cuda", generator=g) * 1.5).to(torch.bfloat16)
     cu = i32(torch, [sum(nq[:i]) for i in range(len(nq) + 1)])
@@ -305,8 +310,9 @@ def test_kv4_attn(torch, sa, c):
     o, l, qn, at = f64(out), f64(lse), f64(q), 0
     for b, (n, k) in enumerate(zip(nq, nk)):
         for h in range(Hq):
-            want = S.attention(qn[at:at + n, h], vals[b][0][:, h * Hkv // Hq], vals[b][1][:, h * Hkv // Hq], window, sinks)
-            check_rows(o[at:at + n, h], l[at:at + n, h], want, d, k, "bf16", 2)
+            kh, vh, extra = (x[:, h * Hkv // Hq] for x in vals[b])
+            want = S.attention(qn[at:at + n, h], kh, vh, window, sinks, extra=extra)
+            check_rows(o[at:at + n, h], l[at:at + n, h], want, 132, k, "bf16", 2)
         at += n
     assert (o[at:] == 7).all() and (l[at:] == 7).all()
     again = torch.empty_like(out)
@@ -513,7 +519,7 @@ def test_steps_together(torch, sa):
     cache.pages.fill_(255)
     rope = sa.Rope(64, layout="half")
     ws = sa.workspace(sa.kv4_attn_workspace(cache, Hq), "cuda")
-    past = [[np.zeros((0, Hkv, d)), np.zeros((0, Hkv, d))] for _ in range(B)]
+    past = [[np.zeros((0, Hkv, d))] * 3 for _ in range(B)]
     q_in, k_in = (torch.zeros(140, h, d, dtype=torch.bfloat16, device="cuda") for h in (Hq, Hkv))
     v_in, out = torch.zeros_like(k_in), torch.zeros_like(q_in)
     lse = torch.zeros(140, Hq, device="cuda")
@@ -534,9 +540,11 @@ def test_steps_together(torch, sa):
             rows = slice(at, at + n)
             for i, x in enumerate((kr, v_in)):
                 past[b][i] = np.concatenate([past[b][i], S.values(*S.quantise(f64(x[rows])))])
+            past[b][2] = np.concatenate([past[b][2], 8 * np.repeat(S.quantise(f64(kr[rows]))[1], 32, -1)])
             for h in range(Hq):
-                want = S.attention(qn[rows, h], past[b][0][:, h * Hkv // Hq], past[b][1][:, h * Hkv // Hq], window, sinks)
-                check_rows(o[rows, h], l[rows, h], want, d, len(past[b][0]), "bf16", 2)
+                kh, vh, extra = (x[:, h * Hkv // Hq] for x in past[b])
+                want = S.attention(qn[rows, h], kh, vh, window, sinks, extra=extra)
+                check_rows(o[rows, h], l[rows, h], want, 132, len(past[b][0]), "bf16", 2)
             at += n
         k.turn()
 
