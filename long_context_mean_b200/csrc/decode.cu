@@ -11,7 +11,7 @@
 //  * the work of the whole batch (every sequence, kv head and row tile times its
 //    16 * SUBS-token tiles) is one line of tiles, cut into equal pieces, one per
 //    CTA, whatever the lengths: a ragged batch and one long sequence fill the
-//    GPU alike.  Lengths are read on the device; a piece may hold several
+//    GPU alike; a unit counts as some tiles more than it has (COST).  Lengths are read on the device; a piece may hold several
 //    units (sequence, row tile, kv head) and a unit several pieces.  Units that
 //    lie in one piece are finished there; parts of others go to the workspace
 //    and join_kernel adds them up in a fixed order (no atomics).
@@ -217,6 +217,10 @@ struct Kv4 {
   // tokens and three stages 83 (12 warps) and 87 (16, whose 128 registers spill).
   static constexpr int STAGES = 2, TILES = D / 16;
   static constexpr int CTAS = 3;
+  // What a unit costs beside its tiles, in tiles (its lengths, queries and output
+  // are a chain of memory latencies): without it a piece of many one-token
+  // sequences takes longest, 192 us where 8 takes 104 (16 sequences of 4 to 131,072).
+  static constexpr int COST = 8;
   // Channel of accumulator tile j's row lane / 4 (+ 8 where half).
   static __device__ __forceinline__ int channel(int j, int half, int r) { return 32 * (j >> 1) + 4 * r + 2 * (j & 1) + half; }
   // A row of q in fp16: its values times 2^x, with 2^x chosen so that the
@@ -406,6 +410,7 @@ struct Bf16 {
   static constexpr float kShift = 0.f;
   static __device__ __forceinline__ float gain(int) { return 1.f; }
   static constexpr int CTAS = 2;
+  static constexpr int COST = 8;
   static __device__ __forceinline__ int channel(int j, int half, int r) { return D == 128 ? 64 * half + 8 * r + j : 8 * r + 4 * half + j; }
   struct Q {
     uint32_t part[D / 8];
@@ -529,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
     Unit u;
     int rt, tl;
     sequence<TOK, ROWS>(a, b, u, rt, tl);
-    sum += (int64_t)rt * a.Hkv * tl;
+    sum += (int64_t)rt * a.Hkv * (F::COST + tl);
   }
   int64_t inc = sum;
   for (int o = 1; o < 32; o <<= 1) {
@@ -552,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
       Unit u;
       int rt, tl;
       sequence<TOK, ROWS>(a, b, u, rt, tl);
-      const int64_t n = (int64_t)rt * a.Hkv * tl;
+      const int64_t n = (int64_t)rt * a.Hkv * (F::COST + tl);
       if (start < pos + n) {
         found_b = b;
         found_off = start - pos;
@@ -577,16 +582,20 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
     Unit u;
     int rt, tl;
     sequence<TOK, ROWS>(a, b, u, rt, tl);
-    const int64_t whole = (int64_t)rt * a.Hkv * tl;
+    const int64_t whole = (int64_t)rt * a.Hkv * (F::COST + tl);
     if (off >= whole) {   // next sequence
       off -= whole;
       ++b;
       continue;
     }
-    const int unit = (int)(off / tl), i0 = (int)(off - (int64_t)unit * tl);
+    const int cost = F::COST + tl, unit = (int)(off / cost);
+    const int x0 = (int)(off - (int64_t)unit * cost), x1 = (int)min64(cost, x0 + (end - at));
+    const int i0 = max(0, x0 - F::COST), i1 = max(0, x1 - F::COST);   // the unit's tiles in this piece
+    at += x1 - x0;
+    off += x1 - x0;
+    if (i1 == 0) continue;   // its tiles begin in the next piece
     u.kvh = unit % a.Hkv;
     u.row0 = (unit / a.Hkv) * ROWS;
-    const int i1 = (int)min64(tl, i0 + (end - at));
     const int rows_all = u.n_q * a.group;
 
     const int first = i0 + warp;
@@ -772,13 +781,11 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
       }
     }
     if (begins && !ends) {
-      piece.last = blockIdx.x + (int)((tl - i1 + per - 1) / per);   // every piece but the last one holds `per` tiles
+      piece.last = blockIdx.x + (int)((cost - x1 + per - 1) / per);   // every piece but the last one holds `per` tiles
       piece.b = u.b;
       piece.row0 = u.row0;
       piece.kvh = u.kvh;
     }
-    at += i1 - i0;
-    off += i1 - i0;
     // The rings are filled next by the async proxy, after these generic accesses.
     if (F::kBulk) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
