@@ -50,22 +50,40 @@ struct Cfg {
   static constexpr int CHUNK_BYTES = kTile * 128;
   static constexpr int OFF_KV = 2 * TILE_BYTES;
   static constexpr int OFF_CTL = OFF_KV + kStages * TILE_BYTES;
-  static constexpr int SMEM = OFF_CTL + 512 + 1024;   // + alignment slack
+  static constexpr int SMEM = OFF_CTL + 3072;
 };
 static_assert(Cfg<128>::SMEM <= 227 * 1024, "shared memory above the 227 KB a CTA may use");
+
+// A query tile of a unit.  Its tiles of keys, by their number kt (128 keys
+// each): some row sees some key of kt < sink or from <= kt < to; every row sees
+// every key where kt < whole_to and (kt >= whole_from or kt < whole_sink).
+struct Rows {
+  int32_t bh, row0, first, last;   // head of the batch, first row, positions of the first and last row
+  int32_t live, sink, from, to, whole_sink, whole_from, whole_to;
+};
+// One unit; the producer derives it and the other roles read it from the ring.
+struct Unit {
+  int32_t n;                       // tiles of keys that it visits; -1: no unit is left
+  int32_t sink_tiles, t_lo;        // the sinks' tiles, then from t_lo on
+  int32_t n_q, n_k, kvh;
+  int32_t lo, hi, n_sink;          // keys that some row sees: [0, n_sink) and [lo, hi)
+  Rows rows[2];
+  __device__ __forceinline__ int tile(int t) const { return t < sink_tiles ? t : t_lo + t - sink_tiles; }
+};
+__device__ __forceinline__ bool active(const Rows& r, int kt) { return kt < r.sink || (kt >= r.from && kt < r.to); }
 
 struct Ctl {
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[kStages], kv_empty[kStages];
-  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_free[2];
   uint64_t u_full[4], u_empty[4];
   uint64_t mma_done;
   unsigned long long wait_ns;
   uint32_t tmem_base;
   volatile uint32_t abort;
-  volatile int32_t ring[4];
+  Unit ring[4];
 };
-static_assert(sizeof(Ctl) <= 512, "control block too large");
+static_assert(sizeof(Ctl) <= 3072, "control block too large");
 
 struct Params {
   uint16_t* out;
@@ -81,56 +99,44 @@ struct Params {
   float scale_log2;
 };
 
-// One unit, as every role derives it from its number.
-struct Unit {
-  int32_t bh[2], row0[2];          // the query tiles: head of the batch, first row
-  int32_t first[2], last[2];       // positions of their first and last row
-  bool live[2];
-  int32_t n_q, n_k, kvh;
-  int32_t lo, hi, n_sink;          // keys that some row sees: [0, n_sink) and [lo, hi)
-  int32_t sink_tiles, t_lo, n;     // tiles: the sinks', then from t_lo on
-};
-
-__device__ __forceinline__ Unit unit_at(const Params& p, int i) {
-  Unit u;
+__device__ __forceinline__ void unit_at(const Params& p, int i, Unit& u) {
   const int blocks = p.num_units / p.pairs;
   const int qb = blocks - 1 - i / p.pairs, pair = i % p.pairs;   // the latest rows have the most keys
   const int per = p.by_heads ? p.Hq / 2 : p.Hq;
   const int b = pair / per, h = (pair % per) * (p.by_heads ? 2 : 1);
-  u.n_q = p.q_len ? p.q_len[b] : p.Nq;
-  u.n_k = p.kv_len ? p.kv_len[b] : p.Nk;
-  if (u.n_q < 0 || u.n_q > p.Nq || u.n_k < 0 || u.n_k > p.Nk) {
+  int n_q = p.q_len ? p.q_len[b] : p.Nq, n_k = p.kv_len ? p.kv_len[b] : p.Nk;
+  if (n_q < 0 || n_q > p.Nq || n_k < 0 || n_k > p.Nk) {
     raise_status(p.status, SA_ERR_INVALID_ARG);
-    u.n_q = max(0, min(u.n_q, p.Nq));
-    u.n_k = max(0, min(u.n_k, p.Nk));
+    n_q = max(0, min(n_q, p.Nq));
+    n_k = max(0, min(n_k, p.Nk));
   }
+  u.n_q = n_q;
+  u.n_k = n_k;
   u.kvh = b * p.Hkv + h / (p.Hq / p.Hkv);
-  int hi = 0;
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    u.bh[t] = b * p.Hq + h + (p.by_heads ? t : 0);
-    u.row0[t] = (p.by_heads ? qb : 2 * qb + t) * kTile;
-    u.live[t] = u.row0[t] < u.n_q;
-    u.first[t] = u.n_k - u.n_q + u.row0[t];
-    u.last[t] = u.n_k - u.n_q + min(u.n_q, u.row0[t] + kTile) - 1;
-    if (u.live[t]) hi = max(hi, min(u.n_k, u.last[t] + 1));
+  int hi = 0, lo = 0;
+  for (int w = 0; w < 2; ++w) {
+    Rows& r = u.rows[w];
+    r.bh = b * p.Hq + h + (p.by_heads ? w : 0);
+    r.row0 = (p.by_heads ? qb : 2 * qb + w) * kTile;
+    r.live = r.row0 < n_q;
+    r.first = n_k - n_q + r.row0;
+    r.last = n_k - n_q + min(n_q, r.row0 + kTile) - 1;
+    const int to = r.live ? max(0, r.last + 1) : 0, from = p.window ? max(0, r.first - p.window + 1) : 0;
+    if (w == 0) lo = from;
+    hi = max(hi, to);
+    r.sink = (min(p.sinks, to) + kTile - 1) / kTile;
+    r.from = from / kTile;
+    r.to = (to + kTile - 1) / kTile;
+    r.whole_sink = p.sinks / kTile;
+    r.whole_from = p.window ? (max(0, r.last - p.window + 1) + kTile - 1) / kTile : 0;
+    r.whole_to = max(0, r.first + 1) / kTile;
   }
   u.hi = hi;
-  u.lo = min(p.window ? max(0, u.first[0] - p.window + 1) : 0, hi);
+  u.lo = min(lo, hi);
   u.n_sink = min(p.sinks, u.lo);
   u.sink_tiles = (u.n_sink + kTile - 1) / kTile;
   u.t_lo = max(u.sink_tiles, u.lo / kTile);
   u.n = hi > 0 ? u.sink_tiles + max(0, (hi + kTile - 1) / kTile - u.t_lo) : 0;
-  return u;
-}
-__device__ __forceinline__ int key0(const Unit& u, int t) {
-  return (t < u.sink_tiles ? t : u.t_lo + t - u.sink_tiles) * kTile;
-}
-// Some row of query tile w sees some key of the tile at k0.
-__device__ __forceinline__ bool active(const Params& p, const Unit& u, int w, int k0) {
-  const int hi = min(u.last[w] + 1, u.n_k);
-  const int lo = p.window ? u.first[w] - p.window + 1 : 0;
-  return u.live[w] && (max(k0, lo) < min(k0 + kTile, hi) || k0 < min(p.sinks, hi));
 }
 
 template <int D>
@@ -153,29 +159,34 @@ __device__ void producer(const CUtensorMap* tmQ, const CUtensorMap* tmK, const C
   for (uint32_t j = 0; ok; ++j) {
     const int slot = j & 3;
     if (!(ok = mbar_wait(&c->u_empty[slot], ((j >> 2) & 1) ^ 1, c, p.status))) break;
-    if (i >= p.num_units) i = -1;
-    c->ring[slot] = i;
+    Unit& u = c->ring[slot];
+    const bool some = i < p.num_units;
+    if (some)
+      unit_at(p, i, u);
+    else
+      u.n = -1;
     mbar_arrive(&c->u_full[slot]);
-    if (i < 0) break;
-    const Unit u = unit_at(p, i);
+    if (!some) break;
     // the next unit: the CTAs' first ones are their own numbers
     i = p.num_units > (int)gridDim.x ? (int)gridDim.x + atomicAdd(p.counter, 1) : p.num_units;
-    for (int t = 0; t < u.n && ok; ++t) {
-      const int k0 = key0(u, t);
-      if (!(ok = load(tmK, k0, u.kvh))) break;
+    const int n = u.n, kvh = u.kvh;
+    for (int t = 0; t < n && ok; ++t) {
+      const int k0 = u.tile(t) * kTile;
+      if (!(ok = load(tmK, k0, kvh))) break;
       if (t == 0) {
         for (int w = 0; w < 2 && ok; ++w) {
-          if (!u.live[w]) continue;
+          if (!u.rows[w].live) continue;
           if (!(ok = mbar_wait(&c->q_empty[w], (nq[w] & 1) ^ 1, c, p.status))) break;
           ++nq[w];
           mbar_expect_tx(&c->q_full[w], C::TILE_BYTES);
 #pragma unroll
           for (int x = 0; x < C::CHUNKS; ++x)
-            tma_load_3d(sb + w * C::TILE_BYTES + x * C::CHUNK_BYTES, tmQ, 64 * x, u.row0[w], u.bh[w], &c->q_full[w]);
+            tma_load_3d(sb + w * C::TILE_BYTES + x * C::CHUNK_BYTES, tmQ, 64 * x, u.rows[w].row0, u.rows[w].bh,
+                        &c->q_full[w]);
         }
         if (!ok) break;
       }
-      ok = load(tmV, k0, u.kvh);
+      ok = load(tmV, k0, kvh);
     }
   }
   // The copies issued last have landed before the CTA may exit.
@@ -196,11 +207,9 @@ __device__ void mma_issuer(const Params& p, Ctl* c, uint32_t sb, uint32_t tm) {
   for (uint32_t j = 0; ok; ++j) {
     const int slot = j & 3;
     if (!(ok = mbar_wait(&c->u_full[slot], (j >> 2) & 1, c, p.status))) break;
-    const int i = c->ring[slot];
-    mbar_arrive(&c->u_empty[slot]);
-    if (i < 0) break;
-    const Unit u = unit_at(p, i);
-    if (u.n == 0) continue;
+    const Unit& u = c->ring[slot];
+    const int n = u.n;
+    if (n < 0) break;
     bool some[2] = {false, false};                    // O holds a product of this unit
     auto qk = [&](int w, int t) {
       const uint32_t it = it0 + 2 * t;
@@ -215,50 +224,59 @@ __device__ void mma_issuer(const Params& p, Ctl* c, uint32_t sb, uint32_t tm) {
       }
       umma_commit(&c->s_full[w]);
     };
-    if (!(ok = full(it0))) break;
-    for (int w = 0; w < 2 && ok; ++w) {
-      if (!u.live[w]) continue;
-      if (!(ok = mbar_wait(&c->q_full[w], nq[w] & 1, c, p.status))) break;
-      ++nq[w];
-      if (active(p, u, w, key0(u, 0))) qk(w, 0);
+    if (n > 0) {
+      for (int w = 0; w < 2 && ok; ++w) {
+        if (!u.rows[w].live) continue;
+        if (!(ok = mbar_wait(&c->q_full[w], nq[w] & 1, c, p.status))) break;
+        ++nq[w];
+        if (active(u.rows[w], u.tile(0))) qk(w, 0);
+      }
+      if (!ok || !(ok = full(it0))) break;
+      umma_commit(&c->kv_empty[it0 % kStages]);
     }
-    if (!ok) break;
-    umma_commit(&c->kv_empty[it0 % kStages]);
-    for (int t = 0; t < u.n && ok; ++t) {
-      const int k0 = key0(u, t), k1 = t + 1 < u.n ? key0(u, t + 1) : 0;
+    for (int t = 0; t < n && ok; ++t) {
+      const int kt = u.tile(t), kt1 = t + 1 < n ? u.tile(t + 1) : -1;
       const uint32_t itv = it0 + 2 * t + 1;
       for (int w = 0; w < 2 && ok; ++w) {
-        if (active(p, u, w, k0)) {
+        if (active(u.rows[w], kt)) {
           if (!some[w] && !(ok = mbar_wait(&c->o_free[w], ((nq[w] - 1) & 1) ^ 1, c, p.status))) break;
           if (!(ok = full(itv))) break;
-          if (!(ok = mbar_wait(&c->p_full[w], np[w] & 1, c, p.status))) break;
-          ++np[w];
-          tc_fence_after();
           const uint32_t vbase = sb + C::OFF_KV + (itv % kStages) * C::TILE_BYTES;
+          // P arrives in two halves of 64 keys: the first half's products run
+          // while the second half's exponentials are computed.
+          for (int h = 0; h < 2 && ok; ++h) {
+            if (!(ok = mbar_wait(h ? &c->p_full[w] : &c->p_half[w], np[w] & 1, c, p.status))) break;
+            tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            umma_ts(tm + 256 * w, tm + 256 * w + 128 + kk * 8, desc_sw128(vbase + kk * 2048, C::CHUNK_BYTES, 1024),
-                    idesc_pv, some[w] || kk > 0 ? 1u : 0u);
+            for (int k4 = 0; k4 < 4; ++k4) {
+              const int kk = 4 * h + k4;
+              umma_ts(tm + 256 * w, tm + 256 * w + 128 + kk * 8, desc_sw128(vbase + kk * 2048, C::CHUNK_BYTES, 1024),
+                      idesc_pv, some[w] || kk > 0 ? 1u : 0u);
+            }
+          }
+          if (!ok) break;
+          ++np[w];
           some[w] = true;
         }
-        if (t + 1 < u.n && active(p, u, w, k1)) qk(w, t + 1);
+        if (kt1 >= 0 && active(u.rows[w], kt1)) qk(w, t + 1);
       }
       // (waits that are over unless no query tile needed the K or V tile)
       if (!ok || !(ok = full(itv))) break;
       umma_commit(&c->kv_empty[itv % kStages]);
-      if (t + 1 < u.n) {
+      if (kt1 >= 0) {
         if (!(ok = full(itv + 1))) break;
         umma_commit(&c->kv_empty[(itv + 1) % kStages]);
       }
     }
     for (int w = 0; w < 2 && ok; ++w)
-      if (u.live[w]) {
+      if (n > 0 && u.rows[w].live) {
         // (one wait a unit, so that the barrier's phases and the units go together)
         if (!some[w] && !(ok = mbar_wait(&c->o_free[w], ((nq[w] - 1) & 1) ^ 1, c, p.status))) break;
         umma_commit(&c->q_empty[w]);
         umma_commit(&c->o_full[w]);
       }
-    it0 += 2 * u.n;
+    it0 += 2 * n;
+    mbar_arrive(&c->u_empty[slot]);
   }
   // Every tensor operation issued here has completed before TMEM is released.
   umma_commit(&c->mma_done);
@@ -276,23 +294,25 @@ __device__ void softmax_rows(const Params& p, Ctl* c, uint8_t* smem, uint32_t tm
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, c, p.status));
   };
+  auto arrive = [&](uint64_t* bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
   for (uint32_t j = 0;; ++j) {
     const int slot = j & 3;
     if (!wait(&c->u_full[slot], (j >> 2) & 1)) return;
-    const int i = c->ring[slot];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&c->u_empty[slot]);
-    if (i < 0) return;
-    const Unit u = unit_at(p, i);
-    const int r = u.row0[w] + row;
-    const bool valid = r < u.n_q;
-    const int pos = u.first[w] + row;
+    const Unit& u = c->ring[slot];
+    const Rows& rows = u.rows[w];
+    const int n = u.n;
+    if (n < 0) return;
     float m = -INFINITY, l = 0.f;       // the reference maximum (log2 units) and the sum relative to it
-    for (int t = 0; t < u.n; ++t) {
-      const int k0 = key0(u, t);
-      if (!active(p, u, w, k0)) continue;
-      // V rows that no row of the unit sees
-      if (k0 + kTile > u.hi || (k0 < u.lo && k0 + kTile > u.n_sink)) {
+    for (int t = 0; t < n; ++t) {
+      const int kt = u.tile(t);
+      if (!active(rows, kt)) continue;
+      const bool whole = kt < rows.whole_to && (kt >= rows.whole_from || kt < rows.whole_sink);
+      const int k0 = kt * kTile;
+      if (!whole && (k0 + kTile > u.hi || (k0 < u.lo && k0 + kTile > u.n_sink))) {
+        // V rows that no row of the unit sees
         const uint32_t itv = it0 + 2 * t + 1;
         if (!wait(&c->kv_full[itv % kStages], (itv / kStages) & 1)) return;
         const int key = k0 + row;
@@ -313,10 +333,9 @@ __device__ void softmax_rows(const Params& p, Ctl* c, uint8_t* smem, uint32_t tm
 #pragma unroll
       for (int x = 0; x < kTile / 32; ++x) tmem_ld32(ts + x * 32, s + x * 32);
       tmem_wait_ld();
-      const bool whole = k0 + kTile - 1 <= u.first[w] && k0 + kTile <= u.n_k &&
-                         (p.window == 0 || u.last[w] - k0 < p.window || k0 + kTile <= p.sinks);
       if (!whole) {
-        const int c_hi = min(pos, u.n_k - 1) - k0, c_lo = p.window ? pos - p.window + 1 - k0 : 0, c_s = p.sinks - k0;
+        // (a valid row's position is below n_k)
+        const int c_hi = rows.first + row - k0, c_lo = p.window ? c_hi - p.window + 1 : 0, c_s = p.sinks - k0;
 #pragma unroll
         for (int x = 0; x < kTile; ++x)
           if (x > c_hi || (x < c_lo && x >= c_s)) s[x] = -INFINITY;
@@ -331,65 +350,67 @@ __device__ void softmax_rows(const Params& p, Ctl* c, uint8_t* smem, uint32_t tm
       const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sc;
       float corr = 1.f;
       bool moved = false;
-      if (top > m + kRescale || (m == -INFINITY && top > m)) {
+      if (top > m + kRescale) {         // (m = -inf: any score is above)
         moved = m != -INFINITY;         // (a row that saw nothing so far has O = 0)
         corr = ex2(m - top);
         m = top;
       }
-      const float ref = m == -INFINITY ? 0.f : m;
-      const uint64_t sc2 = pack2(sc, sc), neg2 = pack2(-ref, -ref);
-      uint64_t acc[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) acc[x] = pack2(0.f, 0.f);
       // O's rescale first: S(t)'s arrival tells that P V of the tile before is done.
       if (__any_sync(0xffffffffu, moved)) {
         const float f = moved ? corr : 1.f;
 #pragma unroll 1
-        for (int x = 0; x < D / 32; ++x) {
-          float o[32];
-          tmem_ld32(to + x * 32, o);
+        for (int x = 0; x < D / 16; ++x) {
+          float o[16];
+          tmem_ld16(to + x * 16, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] *= f;
-          tmem_st32(to + x * 32, reinterpret_cast<const uint32_t*>(o));
+          for (int e = 0; e < 16; ++e) o[e] *= f;
+          tmem_st16(to + x * 16, reinterpret_cast<const uint32_t*>(o));
         }
       }
+      const float ref = m == -INFINITY ? 0.f : m;
+      const uint64_t sc2 = pack2(sc, sc), neg2 = pack2(-ref, -ref);
+      uint64_t acc[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        uint32_t pk[32];
+      for (int x = 0; x < 4; ++x) {
+        uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
+        for (int e = 0; e < 16; ++e) {
           float a, b;
-          unpack2(ffma2(pack2(s[64 * x + 2 * e], s[64 * x + 2 * e + 1]), sc2, neg2), a, b);
+          unpack2(ffma2(pack2(s[32 * x + 2 * e], s[32 * x + 2 * e + 1]), sc2, neg2), a, b);
           a = ex2(a);
           b = ex2(b);
-          acc[e & 3] = fadd2(acc[e & 3], pack2(a, b));
+          acc[e & 1] = fadd2(acc[e & 1], pack2(a, b));
           pk[e] = pack_bf16(a, b);
         }
-        tmem_st32(ts + x * 32, pk);
+        tmem_st16(ts + 16 * x, pk);
+        if (x & 1) {
+          tmem_wait_st();
+          tc_fence_before();
+          arrive(x == 1 ? &c->p_half[w] : &c->p_full[w]);
+        }
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c->p_full[w]);
       float a, b;
-      unpack2(fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3])), a, b);
+      unpack2(fadd2(acc[0], acc[1]), a, b);
       l = l * corr + (a + b);
     }
-    it0 += 2 * u.n;
-    if (!u.live[w]) continue;
-    const bool product = u.n > 0;
-    if (product) {
+    it0 += 2 * n;
+    const int r = rows.row0 + row, live = rows.live;
+    const bool valid = r < u.n_q;
+    const int64_t at = (int64_t)rows.bh * p.Nq + r;
+    arrive(&c->u_empty[slot]);
+    if (!live) continue;
+    if (n > 0) {
       if (!wait(&c->o_full[w], no & 1)) return;
       ++no;
       tc_fence_after();
     }
     const float inv = 1.f / l;
-    uint16_t* orow = p.out + ((int64_t)u.bh[w] * p.Nq + r) * D;
+    uint16_t* orow = p.out + at * D;
 #pragma unroll 1
     for (int x = 0; x < D / 32; ++x) {
       float o[32];
-      if (product) {
+      if (n > 0) {
         tmem_ld32(to + x * 32, o);
         tmem_wait_ld();
       }
@@ -406,12 +427,11 @@ __device__ void softmax_rows(const Params& p, Ctl* c, uint8_t* smem, uint32_t tm
         *reinterpret_cast<uint4*>(orow + x * 32 + e * 8) = v;
       }
     }
-    if (product) {
+    if (n > 0) {
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c->o_free[w]);
+      arrive(&c->o_free[w]);
     }
-    if (valid && p.lse) p.lse[(int64_t)u.bh[w] * p.Nq + r] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (valid && p.lse) p.lse[at] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
   }
 }
 
@@ -421,8 +441,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // Shared memory is full to the last 232 bytes: the base itself has to lie on
+  // the swizzle's 1024-byte boundary, as it does without static shared memory.
+  uint8_t* smem = smem_raw;
   const uint32_t sb = smem_u32(smem);
+  if (sb % 1024 != 0) {
+    raise_status(p.status, SA_ERR_CUDA);
+    return;
+  }
   Ctl* c = reinterpret_cast<Ctl*>(smem + C::OFF_CTL);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -430,7 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&c->q_full[w], 1);
       mbar_init(&c->q_empty[w], 1);
       mbar_init(&c->s_full[w], 1);
-      mbar_init(&c->p_full[w], 4);    // one lane of each softmax warp
+      mbar_init(&c->p_half[w], 4);    // one lane of each softmax warp
+      mbar_init(&c->p_full[w], 4);
       mbar_init(&c->o_full[w], 1);
       mbar_init(&c->o_free[w], 4);
     }
@@ -458,14 +485,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = c->tmem_base;
 
-  // 384 x 168 registers at launch; 256 x 216 + 128 x 64 fit in them.
+  // 384 x 168 registers at launch; 256 x 200 + 128 x 96 fit in them.
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     if (warp == 0 && lane == 0) producer<D>(&tmQ, &tmK, &tmV, p, c, sb);
     if (warp == 1 && lane == 0) mma_issuer<D>(p, c, sb, tmem);
     __syncwarp();
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     softmax_rows<D>(p, c, smem, tmem, (warp - 4) >> 2, warp & 3, lane);
   }
   tc_fence_before();
