@@ -196,91 +196,124 @@ __device__ void producer(const CUtensorMap* tmQ, const CUtensorMap* tmK, const C
     mbar_drain(&c->kv_full[j % kStages], (j / kStages) & 1, c->wait_ns);
 }
 
+// The whole warp runs this, so that addresses and descriptors are uniform, and
+// one elected lane issues.  (A single lane that built every descriptor anew
+// took 85 to 110 clocks a product, whose mma takes 64.)
 template <int D>
 __device__ void mma_issuer(const Params& p, Ctl* c, uint32_t sb, uint32_t tm) {
   using C = Cfg<D>;
   constexpr uint32_t idesc_s = make_idesc(kTile, kTile, 0), idesc_pv = make_idesc(kTile, D, 1);
-  uint32_t it0 = 0;                                   // ring position of the unit's first K tile
+  // Descriptors differ in their start address (16-byte units in the low bits) only.
+  const uint64_t q_desc = desc_sw128(sb, 16, 1024), k_desc = desc_sw128(sb + C::OFF_KV, 16, 1024),
+                 v_desc = desc_sw128(sb + C::OFF_KV, C::CHUNK_BYTES, 1024);
+  uint32_t ks = 0, kph = 0;                           // stage and phase of the next K tile
   uint32_t nq[2] = {0, 0}, np[2] = {0, 0};            // units and tiles so far of each query tile
+  const bool leader = elect_one();
   bool ok = true;
-  auto full = [&](uint32_t it) { return mbar_wait(&c->kv_full[it % kStages], (it / kStages) & 1, c, p.status); };
-  for (uint32_t j = 0; ok; ++j) {
-    const int slot = j & 3;
-    if (!(ok = mbar_wait(&c->u_full[slot], (j >> 2) & 1, c, p.status))) break;
-    const Unit& u = c->ring[slot];
-    const int n = u.n;
-    if (n < 0) break;
-    bool some[2] = {false, false};                    // O holds a product of this unit
-    auto qk = [&](int w, int t) {
-      const uint32_t it = it0 + 2 * t;
-      if (!(ok = full(it))) return;
-      tc_fence_after();
-      const uint32_t qbase = sb + w * C::TILE_BYTES, kbase = sb + C::OFF_KV + (it % kStages) * C::TILE_BYTES;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, c, p.status));
+    if (ok) tc_fence_after();
+    return ok;
+  };
+  auto commit = [&](uint64_t* bar) {
+    if (leader) umma_commit(bar);
+  };
+  auto next = [](uint32_t& s, uint32_t& ph) {
+    if (++s == kStages) {
+      s = 0;
+      ph ^= 1;
+    }
+  };
+  auto qk = [&](int w, uint32_t s) {
+    if (leader) {
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        const uint64_t a = desc_sw128(qbase + (kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32, 16, 1024);
-        const uint64_t b = desc_sw128(kbase + (kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32, 16, 1024);
-        umma_ss(tm + 256 * w + 128, a, b, idesc_s, kk > 0 ? 1u : 0u);
+        constexpr uint32_t chunk = C::CHUNK_BYTES / 16;
+        const uint32_t at = (kk >> 2) * chunk + (kk & 3) * 2;
+        umma_ss(tm + 256 * w + 128, q_desc + (w * (C::TILE_BYTES / 16) + at), k_desc + (s * (C::TILE_BYTES / 16) + at),
+                idesc_s, kk > 0 ? 1u : 0u);
       }
       umma_commit(&c->s_full[w]);
-    };
-    if (n > 0) {
-      for (int w = 0; w < 2 && ok; ++w) {
-        if (!u.rows[w].live) continue;
-        if (!(ok = mbar_wait(&c->q_full[w], nq[w] & 1, c, p.status))) break;
-        ++nq[w];
-        if (active(u.rows[w], u.tile(0))) qk(w, 0);
-      }
-      if (!ok || !(ok = full(it0))) break;
-      umma_commit(&c->kv_empty[it0 % kStages]);
     }
-    for (int t = 0; t < n && ok; ++t) {
-      const int kt = u.tile(t), kt1 = t + 1 < n ? u.tile(t + 1) : -1;
-      const uint32_t itv = it0 + 2 * t + 1;
-      for (int w = 0; w < 2 && ok; ++w) {
+    __syncwarp();
+  };
+  for (uint32_t j = 0;; ++j) {
+    const int slot = j & 3;
+    if (!wait(&c->u_full[slot], (j >> 2) & 1)) break;
+    const Unit& u = c->ring[slot];
+    const int n = __shfl_sync(0xffffffffu, u.n, 0);
+    if (n < 0) break;
+    bool some[2] = {false, false};                    // O holds a product of this unit
+    if (n > 0) {
+      if (!wait(&c->kv_full[ks], kph)) break;
+      for (int w = 0; w < 2; ++w) {
+        if (!u.rows[w].live) continue;
+        if (!wait(&c->q_full[w], nq[w] & 1)) break;
+        ++nq[w];
+        if (active(u.rows[w], u.tile(0))) qk(w, ks);
+      }
+      if (!ok) break;
+      commit(&c->kv_empty[ks]);
+      next(ks, kph);
+    }
+    for (int t = 0; t < n; ++t) {
+      const int kt = u.tile(t), kt1 = u.tile(t + 1);
+      const bool more = t + 1 < n;
+      const uint32_t vs = ks, vph = kph;
+      next(ks, kph);
+      for (int w = 0; w < 2; ++w) {
         if (active(u.rows[w], kt)) {
-          if (!some[w] && !(ok = mbar_wait(&c->o_free[w], ((nq[w] - 1) & 1) ^ 1, c, p.status))) break;
-          if (!(ok = full(itv))) break;
-          const uint32_t vbase = sb + C::OFF_KV + (itv % kStages) * C::TILE_BYTES;
+          if (!some[w] && !wait(&c->o_free[w], ((nq[w] - 1) & 1) ^ 1)) break;
+          if (!wait(&c->kv_full[vs], vph)) break;
           // P arrives in two halves of 64 keys: the first half's products run
           // while the second half's exponentials are computed.
-          for (int h = 0; h < 2 && ok; ++h) {
-            if (!(ok = mbar_wait(h ? &c->p_full[w] : &c->p_half[w], np[w] & 1, c, p.status))) break;
-            tc_fence_after();
 #pragma unroll
-            for (int k4 = 0; k4 < 4; ++k4) {
-              const int kk = 4 * h + k4;
-              umma_ts(tm + 256 * w, tm + 256 * w + 128 + kk * 8, desc_sw128(vbase + kk * 2048, C::CHUNK_BYTES, 1024),
-                      idesc_pv, some[w] || kk > 0 ? 1u : 0u);
+          for (int h = 0; h < 2; ++h) {
+            if (!wait(h ? &c->p_full[w] : &c->p_half[w], np[w] & 1)) break;
+            if (leader) {
+#pragma unroll
+              for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                umma_ts(tm + 256 * w, tm + 256 * w + 128 + kk * 8, v_desc + (vs * (C::TILE_BYTES / 16) + kk * 128),
+                        idesc_pv, some[w] || kk > 0 ? 1u : 0u);
             }
+            __syncwarp();
           }
           if (!ok) break;
           ++np[w];
           some[w] = true;
         }
-        if (kt1 >= 0 && active(u.rows[w], kt1)) qk(w, t + 1);
+        if (more && active(u.rows[w], kt1)) {
+          if (!wait(&c->kv_full[ks], kph)) break;
+          qk(w, ks);
+        }
       }
       // (waits that are over unless no query tile needed the K or V tile)
-      if (!ok || !(ok = full(itv))) break;
-      umma_commit(&c->kv_empty[itv % kStages]);
-      if (kt1 >= 0) {
-        if (!(ok = full(itv + 1))) break;
-        umma_commit(&c->kv_empty[(itv + 1) % kStages]);
+      if (!ok || !wait(&c->kv_full[vs], vph)) break;
+      commit(&c->kv_empty[vs]);
+      if (more) {
+        if (!wait(&c->kv_full[ks], kph)) break;
+        commit(&c->kv_empty[ks]);
+        next(ks, kph);
       }
     }
-    for (int w = 0; w < 2 && ok; ++w)
+    if (!ok) break;
+    for (int w = 0; w < 2; ++w)
       if (n > 0 && u.rows[w].live) {
         // (one wait a unit, so that the barrier's phases and the units go together)
-        if (!some[w] && !(ok = mbar_wait(&c->o_free[w], ((nq[w] - 1) & 1) ^ 1, c, p.status))) break;
-        umma_commit(&c->q_empty[w]);
-        umma_commit(&c->o_full[w]);
+        if (!some[w] && !wait(&c->o_free[w], ((nq[w] - 1) & 1) ^ 1)) break;
+        commit(&c->q_empty[w]);
+        commit(&c->o_full[w]);
       }
-    it0 += 2 * n;
-    mbar_arrive(&c->u_empty[slot]);
+    if (!ok) break;
+    __syncwarp();
+    if (leader) mbar_arrive(&c->u_empty[slot]);
   }
   // Every tensor operation issued here has completed before TMEM is released.
-  umma_commit(&c->mma_done);
-  mbar_drain(&c->mma_done, 0, c->wait_ns);
+  if (leader) {
+    umma_commit(&c->mma_done);
+    mbar_drain(&c->mma_done, 0, c->wait_ns);
+  }
+  __syncwarp();
 }
 
 // Query tile w: thread (quarter wq, lane) owns row 32 wq + lane.
@@ -489,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     if (warp == 0 && lane == 0) producer<D>(&tmQ, &tmK, &tmV, p, c, sb);
-    if (warp == 1 && lane == 0) mma_issuer<D>(p, c, sb, tmem);
+    if (warp == 1) mma_issuer<D>(p, c, sb, tmem);
     __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
