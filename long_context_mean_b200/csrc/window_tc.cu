@@ -237,6 +237,12 @@ __device__ void mma_issuer(const Params& p, Ctl* c, uint32_t sb, uint32_t tm) {
     }
     __syncwarp();
   };
+  // Bit w: query tile w is active in tile t of the unit.
+  auto flags = [](const Unit& u, int t) {
+    const int kt = u.tile(t);
+    const uint32_t f = (active(u.rows[0], kt) ? 1u : 0u) | (active(u.rows[1], kt) ? 2u : 0u);
+    return __shfl_sync(0xffffffffu, f, 0);
+  };
   for (uint32_t j = 0;; ++j) {
     const int slot = j & 3;
     if (!wait(&c->u_full[slot], (j >> 2) & 1)) break;
@@ -256,17 +262,20 @@ __device__ void mma_issuer(const Params& p, Ctl* c, uint32_t sb, uint32_t tm) {
       commit(&c->kv_empty[ks]);
       next(ks, kph);
     }
+    // The tensor cores hold two or three products in their queue, so whatever this
+    // warp does between two batches has to be short: tiles are looked up one
+    // ahead, and V and the next K are waited for before P.
+    uint32_t act = n > 0 ? flags(u, 0) : 0, act1 = n > 1 ? flags(u, 1) : 0;
     for (int t = 0; t < n; ++t) {
-      const int kt = u.tile(t), kt1 = u.tile(t + 1);
-      const bool more = t + 1 < n;
       const uint32_t vs = ks, vph = kph;
       next(ks, kph);
+      if (!wait(&c->kv_full[vs], vph)) break;
+      if (t + 1 < n && !wait(&c->kv_full[ks], kph)) break;
+      uint32_t act2 = 0;
+#pragma unroll
       for (int w = 0; w < 2; ++w) {
-        if (active(u.rows[w], kt)) {
+        if (act >> w & 1) {
           if (!some[w] && !wait(&c->o_free[w], ((nq[w] - 1) & 1) ^ 1)) break;
-          if (!wait(&c->kv_full[vs], vph)) break;
-          // P arrives in two halves of 64 keys: the first half's products run
-          // while the second half's exponentials are computed.
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (!wait(h ? &c->p_full[w] : &c->p_half[w], np[w] & 1)) break;
@@ -279,22 +288,22 @@ __device__ void mma_issuer(const Params& p, Ctl* c, uint32_t sb, uint32_t tm) {
             __syncwarp();
           }
           if (!ok) break;
+          if (act1 >> w & 1) qk(w, ks);
           ++np[w];
           some[w] = true;
-        }
-        if (more && active(u.rows[w], kt1)) {
-          if (!wait(&c->kv_full[ks], kph)) break;
+        } else if (act1 >> w & 1) {
           qk(w, ks);
         }
+        if (w == 0 && t + 2 < n) act2 = flags(u, t + 2);
       }
-      // (waits that are over unless no query tile needed the K or V tile)
-      if (!ok || !wait(&c->kv_full[vs], vph)) break;
+      if (!ok) break;
       commit(&c->kv_empty[vs]);
-      if (more) {
-        if (!wait(&c->kv_full[ks], kph)) break;
+      if (t + 1 < n) {
         commit(&c->kv_empty[ks]);
         next(ks, kph);
       }
+      act = act1;
+      act1 = act2;
     }
     if (!ok) break;
     for (int w = 0; w < 2; ++w)
