@@ -3,10 +3,8 @@
 //
 // Codes: 32 neighbouring channels of one token and head share one bf16 scale
 // s = bf16(amax / 7); the code of x is rint(x / s) in [-7, 7], held as code + 8
-// in 4 bits.  x and s have 8 significant bits, so x / s rounded to 24 bits
-// falls on the same side of every rounding border as the exact quotient: the
-// codes are those of exact arithmetic.  A group with an infinity or a NaN gets
-// a NaN scale, so that it reads back as NaN.
+// in 4 bits; the codes are those of exact arithmetic (code8).  A group with an
+// infinity or a NaN gets a NaN scale, so that it reads back as NaN.
 //
 // A subtile is 16 tokens of one head, 576 * d / 32 bytes in one piece, in the
 // order in which the attention kernel's matrix fragments are filled:
@@ -33,102 +31,178 @@ struct RowArgs {
   uint8_t* cache;
   int32_t* status;
   int64_t T, slots_all;
-  int32_t H, lg_page;
+  int32_t H, lg_page, each;
+  int32_t wide;             // the rows lie on 16-byte boundaries (else 8)
 };
+__device__ __forceinline__ uint4 load8(const uint16_t* p) {
+  const uint2 a = __ldg(reinterpret_cast<const uint2*>(p)), b = __ldg(reinterpret_cast<const uint2*>(p + 4));
+  return make_uint4(a.x, a.y, b.x, b.y);
+}
 
+// Byte offsets of a token's 8 channels 8 cc .. 8 cc + 7.
 template <int G>
-struct Place {   // byte offsets of four channels 4 c4 .. 4 c4 + 3 of a token
+struct Place {
   int64_t base;
-  int k, v, ks, vs;
-  __device__ __forceinline__ Place(int64_t slot, int lg_page, int H, int h, int c4) {
-    const int64_t page = slot >> lg_page;
-    const int in = (int)(slot & ((1 << lg_page) - 1)), t = in & 15;
-    base = (((page * H + h) << (lg_page - 4)) + (in >> 4)) * (576 * G);
-    const int g = c4 >> 3, r = c4 & 7, p = t >> 3, t4 = (t & 7) >> 1, hi = t & 1;
-    k = t * 16 * G + (r >> 1) * 4 * G + g * 4 + (r & 1) * 2;
-    v = 256 * G + p * 128 * G + (r * 4 + t4) * 4 * G + g * 4 + hi * 2;
+  int k, v, ks, vs;   // K's 4 bytes; V's first 2 bytes (tokens of a pair lie side by side, the next 4 channels 16 G on)
+  __device__ __forceinline__ Place(int slot, int lg_page, int H, int h, int cc) {
+    const int in = slot & ((1 << lg_page) - 1), t = in & 15;
+    base = ((((int64_t)(slot >> lg_page) * H + h) << (lg_page - 4)) + (in >> 4)) * (576 * G);
+    const int g = cc >> 2, q4 = cc & 3, p = t >> 3, t4 = (t & 7) >> 1, hi = t & 1;
+    k = t * 16 * G + q4 * 4 * G + g * 4;
+    v = 256 * G + p * 128 * G + (2 * q4 * 4 + t4) * 4 * G + g * 4 + hi * 2;
     ks = 512 * G + t * 2 * G + g * 2;
     vs = 544 * G + p * 16 * G + t4 * 4 * G + g * 4 + hi * 2;
   }
 };
 
-__device__ __forceinline__ uint32_t abs_max4(uint2 x) {
-  return max(max(x.x & 0x7FFFu, (x.x >> 16) & 0x7FFFu), max(x.y & 0x7FFFu, (x.y >> 16) & 0x7FFFu));
+// The largest |x| of 8 values as bf16 bits, of the even and the odd ones.
+__device__ __forceinline__ uint32_t abs_max8(const uint4& x) {
+  constexpr uint32_t M = 0x7FFF7FFFu;
+  return __vmaxu2(__vmaxu2(x.x & M, x.y & M), __vmaxu2(x.z & M, x.w & M));
 }
-// Scale of a group from the largest |x| (as bf16 bits, equal in the group's 8 lanes).
+// Scale of a group from the largest |x| (as bf16 bits, equal in the group's 4 lanes).
 __device__ __forceinline__ uint16_t group_scale(uint32_t amax_bits) {
+  // (A product: amax / 7 is never a tie of bf16, whose odd 9-bit numbers times 7 do
+  // not fit amax's 8 bits, and at least 2^-12 relative away from one.)
   if (amax_bits >= 0x7F80u) return 0x7FC0u;
-  return f32_to_bf16_rne(__fdiv_rn(__uint_as_float(amax_bits << 16), 7.0f));
+  return f32_to_bf16_rne(__uint_as_float(amax_bits << 16) * (1.0f / 7.0f));
 }
-__device__ __forceinline__ uint32_t code4(uint2 x, uint16_t scale) {
+__device__ __forceinline__ float reciprocal(float x) {   // to an ulp, for normal results
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// rint(x / s) + 8 of 8 values, 4 bits each, without dividing each: x and s have 8
+// significant bits, so a quotient of 1/2 or more that is not a half integer is at
+// least 1 / 2040 away from one, and x times 1 / s is off by 2^-20 at most.
+// Rounded to multiples of 2^-12 it is therefore a half integer exactly where the
+// true quotient is, and on the same side of it elsewhere.
+__device__ __forceinline__ uint32_t code8(const uint4& x, uint16_t scale) {
   const float s = bf16_to_f32(scale);
-  if (!(s > 0.f)) return 0x8888u;   // zero or NaN scale
-  const uint32_t w[2] = {x.x, x.y};
-  uint32_t r = 0;
+  if (!(s > 0.f)) return 0x88888888u;   // zero or NaN scale
+  float f[8];
+  unpack16(x, uint16_t{}, f);
+  float inv;
+  if (s < 0x1p-60f) {
+    // Room for the reciprocal; a subnormal scale is coarse, and the quotient may pass 7.
+    const float up = s * 0x1p64f, top = 7.f * up;
+    inv = reciprocal(up);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = fminf(fmaxf(f[i] * 0x1p64f, -top), top);
+  } else {
+    inv = reciprocal(s);
+  }
+  // 1.5 2^11: multiples of 2^-12; 1.5 2^23 + 8: integers, with code + 8 in the low
+  // bits.  The words w = 16 w + bits gather the codes and 8 times kOne's bits.
+  constexpr float kGrid = 3072.f, kOne = 12582920.f;
+  constexpr uint32_t kBits = 0x4B400000u * 0x11111111u;
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 7; i >= 0; --i) w = w * 16 + __float_as_uint((fmaf(f[i], inv, kGrid) - kGrid) + kOne);
+  return w - kBits;
+}
+// The 8 values of a word of codes, rounded to bf16: 128 + nibble by an AND-OR, two
+// channels a register, less 136, times the scale.
+__device__ __forceinline__ uint4 values8(uint32_t codes, uint16_t scale) {
+  const uint32_t s2 = scale * 0x00010001u;
+  uint32_t v[4];   // channels i and i + 4
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float f = __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
-    // (a subnormal scale is coarse: the quotient may pass 7, hence the clamp)
-    const int q = max(-7, min(7, __float2int_rn(__fdiv_rn(f, s))));
-    r |= (uint32_t)(q + 8) << (4 * i);
+    const uint32_t x = ((codes >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+    const __nv_bfloat162 c = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), __floats2bfloat162_rn(136.f, 136.f));
+    const __nv_bfloat162 y = __hmul2(c, *reinterpret_cast<const __nv_bfloat162*>(&s2));
+    v[i] = *reinterpret_cast<const uint32_t*>(&y);
   }
-  return r;
-}
-__device__ __forceinline__ uint2 values4(uint32_t codes, uint16_t scale) {
-  const float s = bf16_to_f32(scale);
-  uint32_t w[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float a = (float)((int)((codes >> (8 * i)) & 15u) - 8) * s;
-    const float b = (float)((int)((codes >> (8 * i + 4)) & 15u) - 8) * s;
-    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    w[i] = *reinterpret_cast<uint32_t*>(&h);
-  }
-  return make_uint2(w[0], w[1]);
+  return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[0], v[1], 0x7632),
+                    __byte_perm(v[2], v[3], 0x7632));
 }
 
-// One thread per (token, head, 4 channels); 8 neighbouring lanes share a
-// group.  WRITE: quantise and store; otherwise read back.
+// A warp takes two neighbouring tokens (half warps) and 16 of their chunks of 8
+// channels; 4 neighbouring lanes share a group.  Where the two tokens are a pair
+// of the cache too (slots 2 n and 2 n + 1, as in every run of tokens), their V
+// codes and scales, which lie side by side, are exchanged between the halves and move
+// as 4 bytes, and with 16-byte rows on the other side one access a lane is left of
+// each: bound by HBM.  WRITE: quantise and store; otherwise read back.
+// A warp walks a.each blocks of chunks of its tokens.
 template <int G, bool WRITE>
 __global__ void __launch_bounds__(256) kv4_rows_kernel(const __grid_constant__ RowArgs a) {
-  constexpr int C4 = 8 * G;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int c4 = (int)(i % C4);
-  const int64_t th = i / C4;
-  const int64_t t = th / a.H;
-  const int h = (int)(th - t * a.H);
-  const bool in = t < a.T;   // a group's 8 lanes agree
-  const int64_t slot = in ? a.slots[t] : -1;
+  constexpr int CH = 4 * G, HEADS = 16 / CH;   // heads of a block of 16 chunks
+  const int lane = threadIdx.x & 31, half = lane >> 4;
+  const uint32_t per = (uint32_t)((a.H + HEADS - 1) / HEADS + a.each - 1) / a.each;   // warps of two tokens
+  const uint32_t warp = blockIdx.x * 8 + (threadIdx.x >> 5), pair_no = warp / per;
+  const int64_t t = (int64_t)pair_no * 2 + half;
+  int h = (int)(warp - pair_no * per) * a.each * HEADS + (lane & 15) / CH;
+  const int cc = lane & (CH - 1);
+  const int slot = t < a.T ? a.slots[t] : -1;
   const bool live = slot >= 0 && slot < a.slots_all;
-  if (in && !live && slot != -1) raise_status(a.status, SA_ERR_INVALID_ARG);
-  const Place<G> at(live ? slot : 0, a.lg_page, a.H, h, c4);
+  if (!live && slot != -1) raise_status(a.status, SA_ERR_INVALID_ARG);
+  const int mate = __shfl_xor_sync(0xffffffffu, live ? slot : -2, 16);
+  const bool pair = live && mate == slot + (half ? -1 : 1) && (slot & 1) == half;
+  if (pair_no * 2 >= a.T) return;   // (whole warps)
+  const Place<G> at(live ? slot : 0, a.lg_page, a.H, h, cc);
+  constexpr int NEXT = 16 * G;   // V's next 4 channels
   uint8_t* p = a.cache + at.base;
-  if constexpr (WRITE) {
-    uint2 k = make_uint2(0, 0), v = k;
-    if (live) {
-      k = __ldg(reinterpret_cast<const uint2*>(a.k + t * a.ks[0] + h * a.ks[1] + c4 * 4));
-      v = __ldg(reinterpret_cast<const uint2*>(a.v + t * a.vs[0] + h * a.vs[1] + c4 * 4));
-    }
-    uint32_t m = abs_max4(k), n = abs_max4(v);
+  // The first half warp moves the pair's first 4 channels of V, the second the next 4.
+  const int at_v = pair && half ? at.v - 2 + NEXT : at.v;
+  const uint16_t *k_in = a.k + t * a.ks[0] + h * a.ks[1] + cc * 8, *v_in = a.v + t * a.vs[0] + h * a.vs[1] + cc * 8;
+  uint16_t *k_out = a.ko + t * a.ks[0] + h * a.ks[1] + cc * 8, *v_out = a.vo + t * a.vs[0] + h * a.vs[1] + cc * 8;
+#pragma unroll 2
+  for (int i = 0; i < a.each; ++i) {
+    const bool on = live && h < a.H;   // a group's 4 lanes, and a pair's two, agree
+    if constexpr (WRITE) {
+      uint4 k = make_uint4(0, 0, 0, 0), v = k;
+      if (on) {
+        k = a.wide ? __ldg(reinterpret_cast<const uint4*>(k_in)) : load8(k_in);
+        v = a.wide ? __ldg(reinterpret_cast<const uint4*>(v_in)) : load8(v_in);
+      }
+      uint32_t m = abs_max8(k), n = abs_max8(v);
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      n = max(n, __shfl_xor_sync(0xffffffffu, n, o));
+      for (int o = 1; o < 4; o <<= 1) {
+        m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+        n = __vmaxu2(n, __shfl_xor_sync(0xffffffffu, n, o));
+      }
+      const uint16_t sk = group_scale(max(m & 0xFFFFu, m >> 16)), sv = group_scale(max(n & 0xFFFFu, n >> 16));
+      const uint32_t kc = code8(k, sk), vc = code8(v, sv);
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, half ? vc & 0xFFFFu : vc >> 16, 16);
+      const uint32_t sv2 = __shfl_xor_sync(0xffffffffu, (uint32_t)sv, 16);
+      if (on) {
+        *reinterpret_cast<uint32_t*>(p + at.k) = kc;
+        if ((cc & 3) == 0) *reinterpret_cast<uint16_t*>(p + at.ks) = sk;
+        if (pair) {
+          *reinterpret_cast<uint32_t*>(p + at_v) = half ? got | (vc & 0xFFFF0000u) : (vc & 0xFFFFu) | got << 16;
+          if ((cc & 3) == 0 && !half) *reinterpret_cast<uint32_t*>(p + at.vs) = sv | sv2 << 16;
+        } else {
+          *reinterpret_cast<uint16_t*>(p + at.v) = (uint16_t)vc;
+          *reinterpret_cast<uint16_t*>(p + at.v + NEXT) = (uint16_t)(vc >> 16);
+          if ((cc & 3) == 0) *reinterpret_cast<uint16_t*>(p + at.vs) = sv;
+        }
+      }
+      k_in += HEADS * a.ks[1];
+      v_in += HEADS * a.vs[1];
+    } else {
+      uint32_t kc = 0, mine = 0;
+      uint16_t sk = 0, sv = 0;
+      if (on) {
+        kc = __ldg(reinterpret_cast<const uint32_t*>(p + at.k));
+        sk = __ldg(reinterpret_cast<const uint16_t*>(p + at.ks));
+        sv = __ldg(reinterpret_cast<const uint16_t*>(p + at.vs));
+        if (pair)
+          mine = __ldg(reinterpret_cast<const uint32_t*>(p + at_v));
+        else
+          mine = __ldg(reinterpret_cast<const uint16_t*>(p + at.v)) |
+                 (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p + at.v + NEXT)) << 16;
+      }
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, half ? mine & 0xFFFFu : mine >> 16, 16);
+      if (on) {
+        const uint32_t vc = !pair ? mine : half ? got | (mine & 0xFFFF0000u) : (mine & 0xFFFFu) | got << 16;
+        *reinterpret_cast<uint4*>(k_out) = values8(kc, sk);
+        *reinterpret_cast<uint4*>(v_out) = values8(vc, sv);
+      }
+      k_out += HEADS * a.ks[1];
+      v_out += HEADS * a.vs[1];
     }
-    const uint16_t sk = group_scale(m), sv = group_scale(n);
-    if (!live) return;
-    *reinterpret_cast<uint16_t*>(p + at.k) = (uint16_t)code4(k, sk);
-    *reinterpret_cast<uint16_t*>(p + at.v) = (uint16_t)code4(v, sv);
-    if ((c4 & 7) == 0) {
-      *reinterpret_cast<uint16_t*>(p + at.ks) = sk;
-      *reinterpret_cast<uint16_t*>(p + at.vs) = sv;
-    }
-  } else {
-    if (!live) return;
-    const uint2 k = values4(*reinterpret_cast<const uint16_t*>(p + at.k), *reinterpret_cast<const uint16_t*>(p + at.ks));
-    const uint2 v = values4(*reinterpret_cast<const uint16_t*>(p + at.v), *reinterpret_cast<const uint16_t*>(p + at.vs));
-    *reinterpret_cast<uint2*>(a.ko + t * a.ks[0] + h * a.ks[1] + c4 * 4) = k;
-    *reinterpret_cast<uint2*>(a.vo + t * a.vs[0] + h * a.vs[1] + c4 * 4) = v;
+    h += HEADS;
+    p += (int64_t)HEADS * (576 * G) << (a.lg_page - 4);
   }
 }
 
@@ -140,10 +214,12 @@ int log2i(int64_t x) {
 
 template <bool WRITE>
 sa_status launch_rows(RowArgs& a, const sa_kv4_desc& d, cudaStream_t st) {
-  const int64_t threads = a.T * d.Hkv * (d.d / 4);
-  const int64_t ctas = ceil_div(threads, 256);
+  // Once two warps an SM sub-partition are there, a warp walks several heads.
+  const int64_t blocks = ceil_div(d.Hkv * (d.d / 8), 16), pairs = ceil_div(a.T, 2);
+  a.each = (int32_t)max64(1, min64(min64(blocks, 8), pairs * blocks / (148 * 8)));
+  const int64_t ctas = ceil_div(pairs * ceil_div(blocks, a.each), 8);
   if (ctas == 0) return SA_OK;
-  if (ctas > 2147483647) return set_error(SA_ERR_UNSUPPORTED, "too many rows");
+  if (ctas > 2147483647 / 8) return set_error(SA_ERR_UNSUPPORTED, "too many rows");
   a.H = (int32_t)d.Hkv;
   a.lg_page = log2i(d.page);
   a.slots_all = d.num_pages * d.page;
@@ -361,6 +437,8 @@ sa_status launch_kv4_append(const void* k, const void* v, int64_t T, const int64
   a.cache = static_cast<uint8_t*>(cache);
   a.status = status;
   a.T = T;
+  a.wide = (uintptr_t)k % 16 == 0 && (uintptr_t)v % 16 == 0;
+  for (int i = 0; i < 2; ++i) a.wide = a.wide && ks[i] % 8 == 0 && vs[i] % 8 == 0;
   return launch_rows<true>(a, d, st);
 }
 
