@@ -490,12 +490,17 @@ typedef struct {
  * d up to 256 with d * elem_size a multiple of 16, on the CUDA cores.  All
  * tensors 16-byte aligned; lse is nullable; out overlaps no input.  ws:
  * sa_window_attn_workspace() bytes (0 for an invalid shape), 256-byte aligned;
- * calls that share it must not overlap on the GPU, captured ones included. */
+ * calls that share it must not overlap on the GPU, captured ones included.
+ * flags: 0, or one of SA_FLAG_FORCE_SIMT, SA_FLAG_FORCE_DECODE,
+ * SA_FLAG_FORCE_PREFILL to choose the kernel where several apply (testing;
+ * SA_ERR_UNSUPPORTED where the chosen one does not). */
+#define SA_FLAG_FORCE_DECODE 8    /* the tensor-core kernel that splits the keys over the GPU */
+#define SA_FLAG_FORCE_PREFILL 16  /* the tensor-core kernel of 128-row tiles */
 size_t sa_window_attn_workspace(const sa_window_shape* shape);
 sa_status sa_window_attn(const void* q, const void* k, const void* v, const sa_window_shape* shape,
                          int64_t window, int64_t sinks, const int32_t* q_len, const int32_t* kv_len,
                          float scale, void* out, float* lse, int32_t* status, void* ws, size_t ws_bytes,
-                         void* stream);
+                         int32_t flags, void* stream);
 
 /* ---- the paged 4-bit cache -----------------------------------------------
  * uint8 [num_pages][Hkv][page / 16][18 * d], 16-byte aligned; page in {16, 32,

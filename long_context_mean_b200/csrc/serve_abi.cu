@@ -9,7 +9,6 @@ using namespace sa;
 namespace {
 
 constexpr int64_t kInt32 = INT32_MAX;
-constexpr int64_t kPrefillRows = 64;   // rows of a sequence from which the prefill kernel is used
 
 bool aligned(const void* p, uintptr_t n) { return (uintptr_t)p % n == 0; }
 
@@ -35,6 +34,19 @@ sa_status check_window_shape(const sa_window_shape* s) {
 }
 
 bool on_tensor_cores(const sa_window_shape& s) { return s.dtype == SA_BF16 && (s.d == 64 || s.d == 128); }
+
+// Which of the two tensor-core kernels takes a shape.  The decode kernel splits
+// every row tile's keys over the GPU: its time goes with the 16-row tiles of all
+// kv heads times the keys, 5.7e-5 us each.  The prefill kernel's goes with the waves
+// of its 256-row units times the 128-key tiles, 1.9 us each.  So it wins above 260
+// row tiles a wave, whatever the keys: 32 query and 8 kv heads over 4096 keys, 128 new
+// tokens 68.7 (decode) and 70.4 us (prefill), 256 tokens 127 and 71; 24 heads of
+// their own, 4 sequences, 32 tokens 55 and 58, 64 tokens 100 and 58.
+bool prefill_wins(const sa_window_shape& s) {
+  const int64_t group = s.Hq / s.Hkv, tiles = ceil_div(s.Nq, 128);
+  const int64_t units = s.B * (group % 2 == 0 ? s.Hq / 2 * tiles : s.Hq * ceil_div(tiles, 2));
+  return s.B * s.Hkv * ceil_div(s.Nq * group, 16) > 260 * ceil_div(units, 148);
+}
 
 sa_status check_kv4(const sa_kv4_desc* d) {
   if (!d) return set_error(SA_ERR_INVALID_ARG, "the cache description is NULL");
@@ -84,7 +96,7 @@ size_t sa_window_attn_workspace(const sa_window_shape* shape) {
 
 sa_status sa_window_attn(const void* q, const void* k, const void* v, const sa_window_shape* shape, int64_t window,
                          int64_t sinks, const int32_t* q_len, const int32_t* kv_len, float scale, void* out,
-                         float* lse, int32_t* status, void* ws, size_t ws_bytes, void* stream) {
+                         float* lse, int32_t* status, void* ws, size_t ws_bytes, int32_t flags, void* stream) {
   if (sa_status e = check_window_shape(shape)) return e;
   if (!q || !k || !v || !out) return set_error(SA_ERR_INVALID_ARG, "NULL tensor argument");
   if (sa_status e = check_window(window, sinks, scale)) return e;
@@ -101,13 +113,17 @@ sa_status sa_window_attn(const void* q, const void* k, const void* v, const sa_w
   const size_t need = sa_window_attn_workspace(shape);
   if (!ws || ws_bytes < need || !aligned(ws, 256))
     return set_error(SA_ERR_WORKSPACE, "sa_window_attn needs %zu bytes of 256-byte aligned workspace", need);
+  if (flags != 0 && flags != SA_FLAG_FORCE_SIMT && flags != SA_FLAG_FORCE_DECODE && flags != SA_FLAG_FORCE_PREFILL)
+    return set_error(SA_ERR_INVALID_ARG, "unknown flags");
+  if (flags > SA_FLAG_FORCE_SIMT && !on_tensor_cores(s))
+    return set_error(SA_ERR_UNSUPPORTED, "no tensor-core kernel for this shape");
   if (sa_status e = check_device()) return e;
   if (!is_sm100()) return set_error(SA_ERR_UNSUPPORTED, "sa_window_attn needs an sm_100 device");
   WindowArgs a{q, k, v, out, lse, q_len, kv_len, status, s, window, sinks,
                scale > 0.f ? scale : 1.0f / std::sqrt((float)s.d), ws};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (!on_tensor_cores(s)) return launch_window_simt(a, st);
-  return s.Nq >= kPrefillRows ? launch_window_tc(a, st) : launch_window_decode(a, st);
+  if (!on_tensor_cores(s) || flags == SA_FLAG_FORCE_SIMT) return launch_window_simt(a, st);
+  return flags == SA_FLAG_FORCE_PREFILL || (flags == 0 && prefill_wins(s)) ? launch_window_tc(a, st) : launch_window_decode(a, st);
 }
 
 size_t sa_kv4_bytes(const sa_kv4_desc* desc) { return check_kv4(desc) == SA_OK ? kv4_size(*desc) : 0; }

@@ -25,7 +25,7 @@ SA_OK, SA_ERR_INVALID_ARG, SA_ERR_UNSUPPORTED, SA_ERR_WORKSPACE = 0, 1, 2, 3
 SA_ERR_EMPTY_ROW, SA_ERR_TIMEOUT, SA_ERR_CUDA, SA_ERR_CAPACITY = 4, 5, 6, 7
 SA_BF16, SA_FP32 = 0, 1
 SA_ORDER = {"identity": 0, "window": 1, "hilbert": 2}
-SA_FLAG_FORCE_SIMT = 1
+SA_FLAG_FORCE_SIMT, SA_FLAG_FORCE_DECODE, SA_FLAG_FORCE_PREFILL = 1, 8, 16
 
 STATUS_NAMES = {0: "SA_OK", 1: "SA_ERR_INVALID_ARG", 2: "SA_ERR_UNSUPPORTED", 3: "SA_ERR_WORKSPACE",
                 4: "SA_ERR_EMPTY_ROW", 5: "SA_ERR_TIMEOUT", 6: "SA_ERR_CUDA", 7: "SA_ERR_CAPACITY"}
@@ -164,7 +164,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "sa_forward_host": (I32, [P, P, P, P, P, ctypes.POINTER(Shape), ctypes.POINTER(LayoutDesc),
                                   ctypes.POINTER(MaskParams), F, F, I32, P, SZ, P, ctypes.POINTER(P * 3)]),
         "sa_window_attn_workspace": (SZ, [ctypes.POINTER(WindowShape)]),
-        "sa_window_attn": (I32, [P, P, P, ctypes.POINTER(WindowShape), I64, I64, P, P, F, P, P, P, P, SZ, P]),
+        "sa_window_attn": (I32, [P, P, P, ctypes.POINTER(WindowShape), I64, I64, P, P, F, P, P, P, P, SZ, I32,
+                                P]),
         "sa_kv4_bytes": (SZ, [ctypes.POINTER(KV4Desc)]),
         "sa_kv4_append": (I32, [P, P, I64, ctypes.POINTER(I64 * 2), ctypes.POINTER(I64 * 2), P,
                                 ctypes.POINTER(KV4Desc), P, P, P]),
@@ -499,7 +500,7 @@ def window_attn_workspace(q, k, v) -> int:
 
 
 def window_attn(q, k, v, out, lse=None, *, window=0, sinks=0, q_len=None, kv_len=None, scale=0.0, status=None,
-                ws=None, stream=None):
+                ws=None, flags=0, stream=None):
     """Causal attention in which a query sees the last `window` keys (0: all)
     and the first `sinks` ones: q, out [B, Hq, Nq, d], k, v [B, Hkv, Nk, d], lse
     [B, Hq, Nq] float32.  Row i of a sequence with n_q rows and n_k keys
@@ -522,7 +523,7 @@ def window_attn(q, k, v, out, lse=None, *, window=0, sinks=0, q_len=None, kv_len
         ws = workspace(load().sa_window_attn_workspace(ctypes.byref(shape)), dev)
     _on(dev, stream, load().sa_window_attn, q.data_ptr(), k.data_ptr(), v.data_ptr(), ctypes.byref(shape), int(window),
         int(sinks), _index(q_len, B, "q_len", dev), _index(kv_len, B, "kv_len", dev), float(scale), out.data_ptr(),
-        _at(lse), _index(status, 1, "status", dev), *_ws_args(ws))
+        _at(lse), _index(status, 1, "status", dev), *_ws_args(ws), int(flags))
 
 
 class KV4Cache:

@@ -104,9 +104,15 @@ def window_inputs(torch, c, seed=0):
     return q, k, v, ql or [Nq] * B, kl or [Nk] * B
 
 
-@pytest.mark.parametrize("c", WINDOW, ids=lambda c: "-".join(map(str, c[:9])))
+def paths(c):
+    """The kernels that a case can be sent to: the library's own choice, the decode, prefill and CUDA-core ones."""
+    return [0, 8, 16, 1] if c[6] == "bf16" and c[5] in (64, 128) else [0]
+
+
+@pytest.mark.parametrize("c,flags", [(c, f) for c in WINDOW for f in paths(c)],
+                         ids=lambda x: str(x) if isinstance(x, int) else "-".join(map(str, x[:9])))
 @pytest.mark.parametrize("poison", [False, True])
-def test_window_attn(torch, sa, c, poison):
+def test_window_attn(torch, sa, c, flags, poison):
     B, Hq, Hkv, Nq, Nk, d, dtype, window, sinks, ql, kl = c
     q, k, v, nq, nk = window_inputs(torch, c)
     if poison:   # whatever no row sees may be anything, and rows behind a sequence too
@@ -121,69 +127,78 @@ def test_window_attn(torch, sa, c, poison):
     ws = sa.workspace(sa.window_attn_workspace(q, k, v), "cuda")
     ws.fill_(255)
     sa.window_attn(q, k, v, out, lse, window=window, sinks=sinks, q_len=ql and i32(torch, ql),
-                   kv_len=kl and i32(torch, kl), status=status, ws=ws)
+                   kv_len=kl and i32(torch, kl), status=status, ws=ws, flags=flags)
     assert sa.read_status(status) == 0
     o, l, qn, kn, vn = (f64(t) for t in (out, lse, q, k, v))
     for b in range(B):
         for h in range(Hq):
             want = S.attention(qn[b, h, :nq[b]], kn[b, h * Hkv // Hq, :nk[b]], vn[b, h * Hkv // Hq, :nk[b]], window, sinks)
-            check_rows(o[b, h, :nq[b]], l[b, h, :nq[b]], want, d, nk[b], dtype, 1 if dtype == "bf16" else 0)
+            check_rows(o[b, h, :nq[b]], l[b, h, :nq[b]], want, d, nk[b], dtype,
+                       1 if dtype == "bf16" and d in (64, 128) and flags != 1 else 0)
         assert (o[b, :, nq[b]:] == 7).all() and (l[b, :, nq[b]:] == 7).all()
     again = torch.full_like(out, 7.0)
-    sa.window_attn(q, k, v, again, window=window, sinks=sinks, q_len=ql and i32(torch, ql), kv_len=kl and i32(torch, kl))
+    sa.window_attn(q, k, v, again, window=window, sinks=sinks, q_len=ql and i32(torch, ql), kv_len=kl and i32(torch, kl),
+                   flags=flags)
     assert torch.equal(again, out)
 
 
-def test_window_attn_bad_lengths_stay_inside(torch, sa):
-    for c in (WINDOW[1], WINDOW[8], WINDOW[19]):
-        q, k, v, nq, nk = window_inputs(torch, c)
-        B = q.shape[0]
-        status = i32(torch, [0])
-        out = torch.empty_like(q)
-        sa.window_attn(q, k, v, out, window=9, kv_len=i32(torch, [1 << 30] + [-5] * (B - 1)), status=status)
-        assert sa.read_status(status) == sa.SA_ERR_INVALID_ARG
-        status.zero_()
-        sa.window_attn(q, k, v, out, window=9, q_len=i32(torch, [-1] + [1 << 30] * (B - 1)), status=status)
-        assert sa.read_status(status) == sa.SA_ERR_INVALID_ARG
+@pytest.mark.parametrize("c,flags", [(WINDOW[1], 8), (WINDOW[8], 16), (WINDOW[8], 8), (WINDOW[19], 0)], ids=str)
+def test_window_attn_bad_lengths_stay_inside(torch, sa, c, flags):
+    q, k, v, nq, nk = window_inputs(torch, c)
+    B = q.shape[0]
+    status = i32(torch, [0])
+    out = torch.empty_like(q)
+    sa.window_attn(q, k, v, out, window=9, kv_len=i32(torch, [1 << 30] + [-5] * (B - 1)), status=status,
+                   flags=flags)
+    assert sa.read_status(status) == sa.SA_ERR_INVALID_ARG
+    status.zero_()
+    sa.window_attn(q, k, v, out, window=9, q_len=i32(torch, [-1] + [1 << 30] * (B - 1)), status=status,
+                   flags=flags)
+    assert sa.read_status(status) == sa.SA_ERR_INVALID_ARG
 
 
-def test_window_attn_scale_and_large_scores(torch, sa):
+@pytest.mark.parametrize("flags", [8, 16, 1])
+def test_window_attn_scale_and_large_scores(torch, sa, flags):
     c = (1, 2, 1, 140, 140, 128, "bf16", 90, 2, None, None)
     q, k, v, _, _ = window_inputs(torch, c)
     q *= 8
     out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
-    sa.window_attn(q, k, v, out, lse, window=90, sinks=2, scale=0.3)
+    sa.window_attn(q, k, v, out, lse, window=90, sinks=2, scale=0.3, flags=flags)
     o, l, qn, kn, vn = (f64(t) for t in (out, lse, q, k, v))
     for h in range(2):
         check_rows(o[0, h], l[0, h], S.attention(qn[0, h], kn[0, 0], vn[0, 0], 90, 2, 0.3), 128, 140, "bf16", 1)
 
 
-def test_window_attn_nan_in_a_visible_key_shows(torch, sa):
-    for c in (WINDOW[0], WINDOW[7], WINDOW[20]):
-        q, k, v, _, _ = window_inputs(torch, c)
-        v[0, 0, 3, 5] = math.nan
-        out = torch.zeros_like(q)
-        sa.window_attn(q, k, v, out)
-        assert torch.isnan(out[0, 0, -1, 5]) and not torch.isnan(out[0, 0, -1, 6])
-        assert not torch.isnan(out[0, -1]).any() or q.shape[1] // k.shape[1] > q.shape[1] - 1
+@pytest.mark.parametrize("c,flags", [(WINDOW[0], 8), (WINDOW[7], 8), (WINDOW[7], 16), (WINDOW[20], 0)], ids=str)
+def test_window_attn_nan_in_a_visible_key_shows(torch, sa, c, flags):
+    q, k, v, _, _ = window_inputs(torch, c)
+    v[0, 0, 3, 5] = math.nan
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:3], device="cuda")
+    sa.window_attn(q, k, v, out, lse, flags=flags)
+    assert torch.isnan(out[0, 0, -1, 5]) and not torch.isnan(out[0, 0, -1, 6])
+    k[0, 0, 2] = math.nan
+    sa.window_attn(q, k, v, out, lse, flags=flags)
+    assert torch.isnan(out[0, 0, -1]).all() and torch.isnan(lse[0, 0, -1])
+    if q.shape[0] > 1:
+        assert torch.isfinite(out[1]).all()
 
 
-@pytest.mark.parametrize("c", [WINDOW[2], WINDOW[8], WINDOW[19]], ids=["decode", "prefill", "fp32"])
-def test_window_attn_other_stream_and_graph(torch, sa, c):
+@pytest.mark.parametrize("c,flags", [(WINDOW[2], 8), (WINDOW[8], 16), (WINDOW[19], 0)], ids=["decode", "prefill", "fp32"])
+def test_window_attn_other_stream_and_graph(torch, sa, c, flags):
     B, Hq, Hkv, Nq, Nk, d, dtype, window, sinks, ql, kl = c
     q, k, v, _, _ = window_inputs(torch, c)
     want = torch.empty_like(q)
-    sa.window_attn(q, k, v, want, window=window, sinks=sinks)
+    sa.window_attn(q, k, v, want, window=window, sinks=sinks, flags=flags)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     got = torch.empty_like(q)
     ws = sa.workspace(sa.window_attn_workspace(q, k, v), "cuda")
-    sa.window_attn(q, k, v, got, window=window, sinks=sinks, ws=ws, stream=side)
+    sa.window_attn(q, k, v, got, window=window, sinks=sinks, ws=ws, stream=side, flags=flags)
     side.synchronize()
     assert torch.equal(got, want)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        sa.window_attn(q, k, v, got, window=window, sinks=sinks, ws=ws)
+        sa.window_attn(q, k, v, got, window=window, sinks=sinks, ws=ws, flags=flags)
     got.zero_()
     graph.replay()
     assert torch.equal(got, want)
@@ -191,7 +206,7 @@ def test_window_attn_other_stream_and_graph(torch, sa, c):
     for a, b in ((q, q2), (k, k2), (v, v2)):
         a.copy_(b)
     graph.replay()
-    sa.window_attn(q2, k2, v2, want, window=window, sinks=sinks)
+    sa.window_attn(q2, k2, v2, want, window=window, sinks=sinks, flags=flags)
     assert torch.equal(got, want)
 
 

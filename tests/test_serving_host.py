@@ -33,13 +33,13 @@ def lib():
 # Refusals
 # ---------------------------------------------------------------------------
 
-def window_code(lib, shape=(2, 4, 2, 5, 70, 128, sa.SA_BF16), window=8, sinks=1, scale=0.0, ws_bytes=None, **kw):
+def window_code(lib, shape=(2, 4, 2, 5, 70, 128, sa.SA_BF16), window=8, sinks=1, scale=0.0, ws_bytes=None, flags=0, **kw):
     s = sa.WindowShape(*shape, 0)
     p = dict(q=at(0), k=at(64), v=at(128), out=at(192), lse=at(256), ws=at(320))
     p.update(kw)
     n = lib.sa_window_attn_workspace(ctypes.byref(s)) if ws_bytes is None else ws_bytes
     return lib.sa_window_attn(p["q"], p["k"], p["v"], ctypes.byref(s), window, sinks, NULL, NULL, scale, p["out"],
-                              p["lse"], NULL, p["ws"], n, NULL)
+                              p["lse"], NULL, p["ws"], n, flags, NULL)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -50,7 +50,8 @@ def window_code(lib, shape=(2, 4, 2, 5, 70, 128, sa.SA_BF16), window=8, sinks=1,
     (dict(scale=math.nan), BAD), (dict(scale=math.inf), BAD), (dict(q=NULL), BAD), (dict(out=NULL), BAD),
     (dict(q=ctypes.c_void_p(0x100000008)), BAD), (dict(out=at(0)), BAD), (dict(out=at(64)), BAD),
     (dict(lse=at(192)), BAD), (dict(ws=NULL), WS), (dict(ws_bytes=100), WS),
-    (dict(ws=ctypes.c_void_p(0x100000080)), WS)])
+    (dict(ws=ctypes.c_void_p(0x100000080)), WS), (dict(flags=2), BAD),
+    (dict(flags=sa.SA_FLAG_FORCE_PREFILL, shape=(2, 4, 2, 5, 70, 128, 1)), UNSUP)])
 def test_window_attn_refusals(lib, kw, code):
     assert window_code(lib, **kw) == code
 
