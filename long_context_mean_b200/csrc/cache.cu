@@ -282,6 +282,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     bad_code = 0;
   }
   __syncthreads();
+  const int64_t count = *a.free_in;   // (with the lengths, not after them)
   const int b0 = min(a.B, tid * a.per), b1 = min(a.B, b0 + a.per);
   int64_t s[3] = {0, 0, 0};
   for (int b = b0; b < b1; ++b) {
@@ -325,7 +326,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       if (w == warp) x[c] += total[c];
       total[c] += part[c][w];
     }
-  const int64_t count = *a.free_in;
   if (tid == 0) {
     int code = 0;
     if (count < 0 || count > a.num_pages) code = SA_ERR_INVALID_ARG;
@@ -388,36 +388,40 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     }
     return page;
   };
-  for (int64_t t = gtid; t < a.max_tokens; t += gsize) {
-    int32_t slot = -1, pos = 0;
-    if (t < n_tok) {
-      const int b = find(tok, a.B, (int)t);
-      const int64_t old = a.kv_len[b];
-      pos = (int32_t)(old + (t - tok[b]));
-      const int blk = pos >> a.lg_page, held = blocks_of(old, a.lg_page);
-      int32_t page = blk < held ? a.table[(int64_t)b * a.max_blocks + blk] : taken(fresh[b] + blk - held);
-      if (page < 0 || page >= a.num_pages) {
-        raise_status(a.status, SA_ERR_INVALID_ARG);
-        page = -1;
+  // All outputs in one index space, so that their chains of loads run side by
+  // side: released pages, fresh blocks, requests, tokens.
+  const int64_t e1 = n_gone, e2 = e1 + n_fresh, e3 = e2 + a.B + 1, e4 = e3 + a.max_tokens;
+  for (int64_t i = gtid; i < e4; i += gsize) {
+    if (i < e1) {
+      const int32_t page = released((int)i);
+      if (page < 0 || page >= a.num_pages) raise_status(a.status, SA_ERR_INVALID_ARG);
+      a.free_list[count + i] = page;
+    } else if (i < e2) {
+      const int f = (int)(i - e1), b = find(fresh, a.B, f);
+      const int held = blocks_of(a.kv_len[b], a.lg_page);
+      a.table[(int64_t)b * a.max_blocks + held + (f - fresh[b])] = taken(f);
+    } else if (i < e3) {
+      const int b = (int)(i - e2);
+      a.cu_q[b] = tok[b];
+      if (b < a.B) a.new_len[b] = a.q_len[b] < 0 ? 0 : a.kv_len[b] + a.q_len[b];
+    } else {
+      const int64_t t = i - e3;
+      int32_t slot = -1, pos = 0;
+      if (t < n_tok) {
+        const int b = find(tok, a.B, (int)t);
+        const int old = a.kv_len[b];
+        pos = old + ((int)t - tok[b]);
+        const int blk = pos >> a.lg_page, held = blocks_of(old, a.lg_page);
+        int32_t page = blk < held ? a.table[(int64_t)b * a.max_blocks + blk] : taken(fresh[b] + blk - held);
+        if (page < 0 || page >= a.num_pages) {
+          raise_status(a.status, SA_ERR_INVALID_ARG);
+          page = -1;
+        }
+        if (page >= 0) slot = (page << a.lg_page) + (pos & ((1 << a.lg_page) - 1));
       }
-      if (page >= 0) slot = (page << a.lg_page) + (pos & ((1 << a.lg_page) - 1));
+      a.slots[t] = slot;
+      a.positions[t] = pos;
     }
-    a.slots[t] = slot;
-    a.positions[t] = pos;
-  }
-  for (int64_t f = gtid; f < n_fresh; f += gsize) {
-    const int b = find(fresh, a.B, (int)f);
-    const int held = blocks_of(a.kv_len[b], a.lg_page);
-    a.table[(int64_t)b * a.max_blocks + held + (f - fresh[b])] = taken((int)f);
-  }
-  for (int64_t r = gtid; r < n_gone; r += gsize) {
-    const int32_t page = released((int)r);
-    if (page < 0 || page >= a.num_pages) raise_status(a.status, SA_ERR_INVALID_ARG);
-    a.free_list[count + r] = page;
-  }
-  for (int64_t b = gtid; b <= a.B; b += gsize) {
-    a.cu_q[b] = tok[b];
-    if (b < a.B) a.new_len[b] = a.q_len[b] < 0 ? 0 : a.kv_len[b] + a.q_len[b];
   }
   if (gtid == 0) *a.free_out = (int32_t)(top - n_fresh);
 }
@@ -469,9 +473,10 @@ sa_status launch_plan(const int32_t* kv_len, const int32_t* q_len, const sa_plan
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return set_error(SA_ERR_CUDA, "cudaFuncSetAttribute(plan_kernel) failed");
-  // One CTA per 2048 outputs: every CTA repeats the scan, so more of them only
-  // pay once there is that much to write.
-  const int64_t want = ceil_div(max64(d.max_tokens, d.B), 4 * kPlanThreads);
+  // Every CTA repeats the scan, which costs the others nothing; how many pages are
+  // released and taken is not known here, so some CTAs are there for them (256
+  // requests of up to 16,000 tokens: 4.4 us, with one CTA 9.2).
+  const int64_t want = max64(8, ceil_div(max64(d.max_tokens, d.B), 2 * kPlanThreads));
   plan_kernel<<<(unsigned)min64(want, 148), kPlanThreads, smem, st>>>(a);
   return check_launch("plan_kernel");
 }

@@ -445,7 +445,8 @@ def _need(ok, msg):
 def _same(t, dtype, shape, name, device, contiguous=True):
     """t is a CUDA tensor of this dtype, shape and device."""
     try:
-        if (t.dtype is dtype and t.device == device and t.is_cuda and t.shape == shape
+        # (get_device() is -1 on the CPU, where device.index is None)
+        if (t.dtype is dtype and t.get_device() == device.index and t.shape == shape
                 and (not contiguous or t.is_contiguous())):
             return
     except AttributeError:
@@ -457,12 +458,18 @@ def _same(t, dtype, shape, name, device, contiguous=True):
     _need(False, f"{name} must be contiguous")
 
 
+_int32 = None   # torch.int32, once torch is imported
+
+
 def _index(t, n, name, device):
     """The address of an int32 [n] argument, or None."""
     if t is None:
         return None
-    import torch
-    _same(t, torch.int32, (n,), name, device)
+    global _int32
+    if _int32 is None:
+        import torch
+        _int32 = torch.int32
+    _same(t, _int32, (n,), name, device)
     return t.data_ptr()
 
 
