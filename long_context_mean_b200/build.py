@@ -4,7 +4,8 @@
 an object (in parallel, only when a source or header is newer than its
 object) and links them into ``long_context_mean_b200/libsparseattn.so``.
 The CUDA runtime is linked statically; no libcuda link is needed (driver
-entry points are fetched at run time).
+entry points are fetched at run time).  ``csrc/binding.cpp`` becomes
+``_serve.so``, the compiled Python binding of the serving operators.
 """
 
 from __future__ import annotations
@@ -22,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsparseattn.so")
+BINDING = os.path.join(PKG, "_serve.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -55,6 +57,30 @@ def _compile(src: str, extra: list[str], verbose: bool) -> str:
     return obj
 
 
+def build_binding(verbose: bool = False) -> str:
+    """The compiled Python binding of the serving operators (csrc/binding.cpp, host code against torch's headers)."""
+    src = os.path.join(CSRC, "binding.cpp")
+    if os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(src), _newest_header()):
+        return BINDING
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    inc = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], INCLUDE,
+           os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-DTORCH_EXTENSION_NAME=_serve", *[x for d in inc for x in ("-isystem", d)], src, "-o", BINDING + ".tmp",
+           "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
+
+
 def build(verbose: bool = False, extra: list[str] | None = None, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     extra = list(extra or [])
@@ -64,8 +90,12 @@ def build(verbose: bool = False, extra: list[str] | None = None, force: bool = F
             o = os.path.join(BUILD, os.path.basename(s)[:-3] + ".o")
             if os.path.exists(o):
                 os.remove(o)
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    if force and os.path.exists(BINDING):
+        os.remove(BINDING)
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        binding = ex.submit(build_binding, verbose)
         objs = list(ex.map(lambda s: _compile(s, extra, verbose), srcs))
+        binding.result()
     if not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
         cmd = [nvcc(), *ARCH, "-shared", "-o", LIB + ".tmp", *objs]
         r = subprocess.run(cmd, capture_output=True, text=True)

@@ -526,8 +526,6 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
 
-  // (join_kernel may take its place on the SMs now; it waits for this grid's end)
-  asm volatile("griddepcontrol.launch_dependents;");
   // Where this piece of the line of tiles starts.
   const int per_thread = (a.B + kThreads - 1) / kThreads;
   const int b0 = min(a.B, tid * per_thread), b1 = min(a.B, b0 + per_thread);

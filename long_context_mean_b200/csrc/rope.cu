@@ -38,6 +38,7 @@ struct RopeArgs {
   float mag;
   int32_t items;                // vector items of one head (pairs of vectors, then copies)
   int32_t pair_items;
+  uint64_t items_inv;           // ceil(2^40 / items): exact quotients, as numbers times items stay below 2^40
 };
 
 template <typename T, int VEC> struct Pack;
@@ -76,14 +77,67 @@ template <typename T> struct Pack<T, 1> {
   static __device__ __forceinline__ void store(T* p, const float* f) { Elem<T>::store(p, f[0]); }
 };
 
+// One item: the vector pair (HALF) or vector of a head's rotated channels, or a
+// vector of those that do not turn.
+template <typename T, int VEC, bool HALF>
+struct Item {
+  static constexpr int W = VEC < 2 ? 2 : VEC;   // interleaved: whole pairs
+  const T* x;
+  T* y;
+  const float2* c;
+  float u[W], v[VEC];
+  int kind;   // 0: nothing, 1: turn, 2: copy
+  __device__ __forceinline__ void load(int half) {
+    if (kind == 0) return;
+    if (HALF || kind == 2) {
+      Pack<T, VEC>::load(x, u);
+      if (kind == 1) Pack<T, VEC>::load(x + half, v);
+    } else {
+      Pack<T, W>::load(x, u);
+    }
+  }
+  __device__ __forceinline__ void store(int half) {
+    if (kind == 0) return;
+    if (kind == 2) {
+      Pack<T, VEC>::store(y, u);
+    } else if constexpr (HALF) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float2 w = c[e];
+        const float p = u[e] * w.x - v[e] * w.y, q = v[e] * w.x + u[e] * w.y;
+        u[e] = p;
+        v[e] = q;
+      }
+      Pack<T, VEC>::store(y, u);
+      Pack<T, VEC>::store(y + half, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < W; e += 2) {
+        const float2 w = c[e >> 1];
+        const float p = u[e] * w.x - u[e + 1] * w.y, q = u[e + 1] * w.x + u[e] * w.y;
+        u[e] = p;
+        u[e + 1] = q;
+      }
+      Pack<T, W>::store(y, u);
+    }
+  }
+};
+
 // x and y may be the same buffer (in place), so loads are plain loads and a
-// thread reads both channels of its pairs before it writes them.
+// thread reads all channels of its pairs before it writes them.
 template <typename T, int VEC, bool HALF, int TOK>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
   extern __shared__ float2 cs[];   // [TOK][rot / 2]
+  __shared__ int64_t at[TOK][4];   // the tokens' places in q, q_out, k, k_out
   const int half = a.rot >> 1;
   const int64_t t0 = (int64_t)blockIdx.x * TOK;
   const int nt = (int)min64(TOK, a.tokens - t0);
+  if (threadIdx.x < nt * 4) {
+    const int tt = threadIdx.x >> 2, z = threadIdx.x & 3;
+    const int64_t t = t0 + tt, b = t / a.N, n = t - b * a.N;
+    const int64_t* s = z & 1 ? a.ys[z >> 1] : a.xs[z >> 1];
+    at[tt][z] = b * s[0] + n * s[1];
+  }
   for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
     const int tt = i / half, f = i - tt * half;
     const int64_t t = t0 + tt, b = t / a.N;
@@ -107,51 +161,32 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     cs[i] = make_float2(c * a.mag, a.inverse ? -s * a.mag : s * a.mag);
   }
   __syncthreads();
-  const int per_tok = a.heads_all * a.items;
-  for (int i = threadIdx.x; i < nt * per_tok; i += kRopeThreads) {
-    const int tt = i / per_tok, r = i - tt * per_tok;
-    int h = r / a.items;
+  const int per_tok = a.heads_all * a.items, all = nt * per_tok;
+  auto item = [&](int i) {
+    Item<T, VEC, HALF> m;
+    m.kind = 0;
+    if (i >= all) return m;
+    int tt = 0;
+#pragma unroll
+    for (int x = 1; x < TOK; ++x) tt += i >= x * per_tok;
+    const int r = i - tt * per_tok;
+    int h = (int)(((uint64_t)r * a.items_inv) >> 40);   // r / items
     const int it = r - h * a.items;
     const int which = h >= a.heads[0];
     if (which) h -= a.heads[0];
-    const int64_t t = t0 + tt, b = t / a.N, n = t - b * a.N;
-    const T* x = static_cast<const T*>(a.x[which]) + b * a.xs[which][0] + n * a.xs[which][1] + h * a.xs[which][2];
-    T* y = static_cast<T*>(a.y[which]) + b * a.ys[which][0] + n * a.ys[which][1] + h * a.ys[which][2];
-    const float2* c = cs + tt * half;
-    if (it >= a.pair_items) {   // channels that do not turn
-      if (!a.copy[which]) continue;
-      const int ch = a.rot + (it - a.pair_items) * VEC;
-      float f[VEC];
-      Pack<T, VEC>::load(x + ch, f);
-      Pack<T, VEC>::store(y + ch, f);
-    } else if constexpr (HALF) {
-      const int ch = it * VEC;
-      float u[VEC], v[VEC];
-      Pack<T, VEC>::load(x + ch, u);
-      Pack<T, VEC>::load(x + half + ch, v);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float2 w = c[ch + e];
-        const float p = u[e] * w.x - v[e] * w.y, q = v[e] * w.x + u[e] * w.y;
-        u[e] = p;
-        v[e] = q;
-      }
-      Pack<T, VEC>::store(y + ch, u);
-      Pack<T, VEC>::store(y + half + ch, v);
-    } else {
-      constexpr int W = VEC < 2 ? 2 : VEC;
-      const int ch = it * W;
-      float u[W];
-      Pack<T, W>::load(x + ch, u);
-#pragma unroll
-      for (int e = 0; e < W; e += 2) {
-        const float2 w = c[(ch + e) >> 1];
-        const float p = u[e] * w.x - u[e + 1] * w.y, q = u[e + 1] * w.x + u[e] * w.y;
-        u[e] = p;
-        u[e + 1] = q;
-      }
-      Pack<T, W>::store(y + ch, u);
-    }
+    const bool turns = it < a.pair_items;
+    if (!turns && !a.copy[which]) return m;
+    const int ch = turns ? it * (HALF ? VEC : Item<T, VEC, HALF>::W) : a.rot + (it - a.pair_items) * VEC;
+    m.kind = turns ? 1 : 2;
+    m.x = static_cast<const T*>(a.x[which]) + at[tt][2 * which] + h * a.xs[which][2] + ch;
+    m.y = static_cast<T*>(a.y[which]) + at[tt][2 * which + 1] + h * a.ys[which][2] + ch;
+    m.c = cs + tt * half + (HALF ? ch : ch >> 1);
+    return m;
+  };
+  for (int i = threadIdx.x; i < all; i += kRopeThreads) {
+    Item<T, VEC, HALF> m = item(i);
+    m.load(half);
+    m.store(half);
   }
 }
 
@@ -159,6 +194,7 @@ template <typename T, int VEC, bool HALF, int TOK>
 sa_status launch_tok(RopeArgs& a, cudaStream_t st) {
   a.pair_items = HALF ? a.rot / 2 / VEC : a.rot / (VEC < 2 ? 2 : VEC);
   a.items = a.pair_items + (a.d - a.rot) / VEC;
+  a.items_inv = (1ull << 40) / a.items + 1;
   const int64_t ctas = ceil_div(a.tokens, TOK);
   if (ctas > 2147483647) return set_error(SA_ERR_UNSUPPORTED, "too many tokens");
   rope_kernel<T, VEC, HALF, TOK><<<(unsigned)ctas, kRopeThreads, (size_t)TOK * (a.rot / 2) * sizeof(float2), st>>>(a);

@@ -435,65 +435,47 @@ def read_status(status, stream=None) -> int:
 # window attention
 # ---------------------------------------------------------------------------
 # These take tensors of any one device (which need not be the current one)
-# and run on `stream`, or on that device's current stream.
+# and run on `stream`, or on that device's current stream.  Their checks and
+# marshalling are compiled (csrc/binding.cpp): a step of single tokens makes
+# its calls for kernels of 4 us, and the checks alone took longer in Python.
+
+_serve = None
+
+
+def _binding():
+    """The compiled binding, with the entry points of the loaded library."""
+    global _serve
+    if _serve is None:
+        lib = load()
+        try:
+            from . import _serve as m
+        except ImportError as e:
+            raise RuntimeError("_serve.so cannot be loaded: build it with `python -m long_context_mean_b200.build` "
+                               f"(there is no fallback implementation): {e}") from e
+        m.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in SERVE_ENTRIES})
+        _serve = m
+    return _serve
+
+
+SERVE_ENTRIES = ["sa_window_attn", "sa_kv4_append", "sa_kv4_read", "sa_kv4_attn", "sa_rope", "sa_cache_plan"]
+
 
 def _need(ok, msg):
     if not ok:
         raise ValueError(msg)
 
 
-def _same(t, dtype, shape, name, device, contiguous=True):
-    """t is a CUDA tensor of this dtype, shape and device."""
-    try:
-        # (get_device() is -1 on the CPU, where device.index is None)
-        if (t.dtype is dtype and t.get_device() == device.index and t.shape == shape
-                and (not contiguous or t.is_contiguous())):
-            return
-    except AttributeError:
-        raise ValueError(f"{name} must be a {dtype} tensor") from None
-    # (the messages are built only here: a step of single tokens makes some thirty of these checks)
-    _need(t.dtype is dtype, f"{name} must be a {dtype} tensor")
-    _need(t.device == device and t.is_cuda, f"{name} must be on the same CUDA device as the other tensors")
-    _need(t.shape == shape, f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    _need(False, f"{name} must be contiguous")
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream
 
 
-_int32 = None   # torch.int32, once torch is imported
-
-
-def _index(t, n, name, device):
-    """The address of an int32 [n] argument, or None."""
-    if t is None:
-        return None
-    global _int32
-    if _int32 is None:
-        import torch
-        _int32 = torch.int32
-    _same(t, _int32, (n,), name, device)
-    return t.data_ptr()
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
-def _on(device, stream, fn, *args):
-    """fn(*args, stream) with `device` current."""
-    import torch
-    if device.index == torch._C._cuda_getDevice():
-        # (the raw stream: torch.cuda.current_stream() takes 3 us, the rest of a call 8)
-        code = fn(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
-    else:
-        with torch.cuda.device(device):
-            code = fn(*args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream)
-    if code != SA_OK:
-        _check(code)
-
-
-def _ws_args(ws):
-    if not ws.is_contiguous():
-        raise ValueError("ws must be contiguous")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+def _call_workspace(nbytes, t, name, stream):
+    """A workspace for one call on tensors like t."""
+    _need(t.is_cuda, f"{name} must be on a CUDA device")
+    ws = workspace(nbytes, t.device)
+    if stream is not None:
+        ws.record_stream(stream)     # it stays allocated until that stream has used it
+    return ws
 
 
 def make_window_shape(q, k) -> WindowShape:
@@ -514,23 +496,11 @@ def window_attn(q, k, v, out, lse=None, *, window=0, sinks=0, q_len=None, kv_len
     sits at position n_k - n_q + i; q_len, kv_len (int32 [B]) are the lengths
     of a padded batch, and rows past q_len stay as they were.  ws: a
     workspace() of window_attn_workspace() bytes (allocated per call if None)."""
-    import torch
-    dev = q.device
-    _need(q.dim() == 4 and k.dim() == 4, "q and k must have four axes")
-    B, Hq, Nq, d = q.shape
-    Hkv, Nk = k.shape[1:3]
-    _same(q, q.dtype, (B, Hq, Nq, d), "q", dev)
-    _same(k, q.dtype, (B, Hkv, Nk, d), "k", dev)
-    _same(v, q.dtype, (B, Hkv, Nk, d), "v", dev)
-    _same(out, q.dtype, (B, Hq, Nq, d), "out", dev)
-    if lse is not None:
-        _same(lse, torch.float32, (B, Hq, Nq), "lse", dev)
-    shape = WindowShape(B, Hq, Hkv, Nq, Nk, d, dtype_code(q), 0)
     if ws is None:
-        ws = workspace(load().sa_window_attn_workspace(ctypes.byref(shape)), dev)
-    _on(dev, stream, load().sa_window_attn, q.data_ptr(), k.data_ptr(), v.data_ptr(), ctypes.byref(shape), int(window),
-        int(sinks), _index(q_len, B, "q_len", dev), _index(kv_len, B, "kv_len", dev), float(scale), out.data_ptr(),
-        _at(lse), _index(status, 1, "status", dev), *_ws_args(ws), int(flags))
+        ws = _call_workspace(window_attn_workspace(q, k, v), q, "q", stream)
+    code = _binding().window_attn(q, k, v, out, lse, window, sinks, q_len, kv_len, scale, status, ws, flags, _raw(stream))
+    if code != SA_OK:
+        _check(code)
 
 
 class KV4Cache:
@@ -539,8 +509,9 @@ class KV4Cache:
 
     def __init__(self, pages, page: int, d: int):
         import torch
-        _need(pages.dim() == 4, "the pages must have four axes")
-        _same(pages, torch.uint8, (*pages.shape[:2], page // 16, 18 * d), "pages", pages.device)
+        _need(pages.dim() == 4 and pages.dtype == torch.uint8 and pages.is_contiguous(),
+              "the pages must be a contiguous uint8 tensor of four axes")
+        _need(tuple(pages.shape[2:]) == (page // 16, 18 * d), "the pages must have shape [num_pages, Hkv, page / 16, 18 d]")
         self.pages, self.page, self.d = pages, int(page), int(d)
         self.num_pages, self.Hkv = pages.shape[:2]
         self.desc = KV4Desc(self.num_pages, self.Hkv, self.page, self.d)
@@ -553,36 +524,19 @@ class KV4Cache:
         return cls(torch.zeros(num_pages, Hkv, page // 16, 18 * d, dtype=torch.uint8, device=device), page, d)
 
 
-_I64x2 = ctypes.c_int64 * 2
-
-
-def _rows_of(t, name, T, H, d, dev):
-    """Strides {token, head} of a bf16 [T, H, d] tensor."""
-    import torch
-    _same(t, torch.bfloat16, (T, H, d), name, dev, contiguous=False)
-    s = t.stride()
-    if s[2] != 1 and d != 1:
-        raise ValueError(f"the channels of {name} must be contiguous")
-    return ctypes.byref(_I64x2(s[0], s[1]))
-
-
 def kv4_append(k, v, slots, cache: KV4Cache, *, status=None, stream=None):
     """Tokens k, v (bf16 [T, Hkv, d]) into the slots of the cache (int32 [T],
     -1 = leave out; the others must differ)."""
-    T, dev = k.shape[0], cache.pages.device
-    ks, vs = _rows_of(k, "k", T, cache.Hkv, cache.d, dev), _rows_of(v, "v", T, cache.Hkv, cache.d, dev)
-    _on(dev, stream, load().sa_kv4_append, k.data_ptr(), v.data_ptr(), T, ks, vs, _index(slots, T, "slots", dev),
-        ctypes.byref(cache.desc), cache.pages.data_ptr(), _index(status, 1, "status", dev))
+    code = _binding().kv4_append(k, v, slots, cache.pages, cache.page, cache.d, status, _raw(stream))
+    if code != SA_OK:
+        _check(code)
 
 
 def kv4_read(cache: KV4Cache, slots, k, v, *, status=None, stream=None):
     """The values of the cache's slots (int32 [T]) into k, v (bf16 [T, Hkv, d])."""
-    import torch
-    T, dev = k.shape[0], cache.pages.device
-    _same(k, torch.bfloat16, (T, cache.Hkv, cache.d), "k", dev)
-    _same(v, torch.bfloat16, (T, cache.Hkv, cache.d), "v", dev)
-    _on(dev, stream, load().sa_kv4_read, cache.pages.data_ptr(), ctypes.byref(cache.desc),
-        _index(slots, T, "slots", dev), T, k.data_ptr(), v.data_ptr(), _index(status, 1, "status", dev))
+    code = _binding().kv4_read(cache.pages, cache.page, cache.d, slots, k, v, status, _raw(stream))
+    if code != SA_OK:
+        _check(code)
 
 
 def kv4_attn_workspace(cache: KV4Cache, Hq: int) -> int:
@@ -596,23 +550,12 @@ def kv4_attn(q, cache: KV4Cache, table, kv_len, out, lse=None, *, cu_q, window=0
     has the tokens cu_q[b] : cu_q[b + 1] (int32 [B + 1]), the last of its
     kv_len[b] (int32 [B]) keys, in the pages table[b] (int32 [B, max_blocks]).
     out bf16 [T, Hq, d], lse float32 [T, Hq]; window and sinks as in window_attn."""
-    import torch
-    dev = cache.pages.device
-    _need(q.dim() == 3 and table.dim() == 2, "q must have three axes and table two")
-    T, Hq = q.shape[:2]
-    qs = _rows_of(q, "q", T, Hq, cache.d, dev)
-    B, max_blocks = table.shape
-    _same(table, torch.int32, (B, max_blocks), "table", dev)
-    _same(out, torch.bfloat16, (T, Hq, cache.d), "out", dev)
-    if lse is not None:
-        _same(lse, torch.float32, (T, Hq), "lse", dev)
     if ws is None:
-        ws = workspace(kv4_attn_workspace(cache, Hq), dev)
-    _need(cu_q is not None and kv_len is not None, "cu_q and kv_len are needed")
-    _on(dev, stream, load().sa_kv4_attn, q.data_ptr(), T, Hq, qs, _index(cu_q, B + 1, "cu_q", dev), B,
-        cache.pages.data_ptr(), ctypes.byref(cache.desc), table.data_ptr(), max_blocks,
-        _index(kv_len, B, "kv_len", dev), int(window), int(sinks), float(scale), out.data_ptr(), _at(lse),
-        _index(status, 1, "status", dev), *_ws_args(ws))
+        ws = _call_workspace(kv4_attn_workspace(cache, q.shape[1]), cache.pages, "the cache", stream)
+    code = _binding().kv4_attn(q, cache.pages, cache.page, cache.d, table, kv_len, out, lse, cu_q, window, sinks, scale,
+                               status, ws, _raw(stream))
+    if code != SA_OK:
+        _check(code)
 
 
 ROPE_LAYOUT = {"half": 0, "interleaved": 1}
@@ -638,16 +581,6 @@ class Rope:
         self.magnitude = float(mag.value)
         self.host_freqs = host              # uint64 bits: turns per position in units of 2^-64
         self.freqs = host.to(device)
-        self.descs = {}                     # descriptions of the calls' sizes and strides
-
-
-def _rope_strides(t, name, shape, dtype, dev):
-    """Strides {batch, token, head} of a [T, H, d] or [B, N, H, d] tensor."""
-    _same(t, dtype, shape, name, dev, contiguous=False)
-    s = t.stride()
-    if s[-1] != 1 and shape[-1] != 1:
-        raise ValueError(f"the channels of {name} must be contiguous")
-    return s[:3] if len(s) == 4 else (0, s[0], s[1])
 
 
 def rope(rope: Rope, pos, q, q_out, k=None, k_out=None, *, inverse=False, stream=None):
@@ -655,32 +588,10 @@ def rope(rope: Rope, pos, q, q_out, k=None, k_out=None, *, inverse=False, stream
     [B, N, H, d] with pos [N] or [B, N]; any strides with contiguous channels)
     into q_out and k_out, which may be q and k.  inverse: turn back, the
     gradient of the forward rotation."""
-    import torch
-    dev, shape, dt = q.device, q.shape, q.dtype
-    _need(len(shape) in (3, 4), "q must have three or four axes")
-    _need((k is None) == (k_out is None), "k and k_out go together")
-    lead, d = shape[:-2], shape[-1]
-    qs, qo = _rope_strides(q, "q", shape, dt, dev), _rope_strides(q_out, "q_out", shape, dt, dev)
-    ks = ko = (0, 0, 0)
-    Hk = 0
-    if k is not None:
-        Hk = k.shape[-2]
-        ks = _rope_strides(k, "k", (*lead, Hk, d), dt, dev)
-        ko = _rope_strides(k_out, "k_out", (*lead, Hk, d), dt, dev)
-    B, N = (1, lead[0]) if len(lead) == 1 else lead
-    batched = pos.dim() == 2 and len(lead) == 2
-    _same(pos, torch.int32, lead if batched else (N,), "pos", dev, contiguous=False)
-    _need(N <= 1 or pos.stride(-1) == 1, "the positions of a sequence must be contiguous")
-    _need(rope.freqs.device == dev, "the frequencies must be on the tensors' device")
-    key = (dt, B, N, shape[-2], Hk, d, qs, qo, ks, ko, pos.stride(0) if batched else 0, bool(inverse))
-    desc = rope.descs.get(key)
-    if desc is None:
-        desc = RopeDesc(*key[1:11], rope.rot_dim, rope.layout, dtype_code(q), int(bool(inverse)), rope.magnitude, 0)
-        if len(rope.descs) >= 64:
-            rope.descs.clear()
-        rope.descs[key] = desc
-    _on(dev, stream, load().sa_rope, q.data_ptr(), q_out.data_ptr(), _at(k), _at(k_out), pos.data_ptr(),
-        rope.freqs.data_ptr(), ctypes.byref(desc))
+    code = _binding().rope(rope.freqs, rope.rot_dim, rope.layout, rope.magnitude, pos, q, q_out, k, k_out, inverse,
+                           _raw(stream))
+    if code != SA_OK:
+        _check(code)
 
 
 def cache_plan(kv_len, q_len, table, free_list, free_count, page, new_len, cu_q, slots, positions, free_count_out, *,
@@ -691,21 +602,10 @@ def cache_plan(kv_len, q_len, table, free_list, free_count, page, new_len, cu_q,
     of them free) in place; writes new_len [B], cu_q [B + 1], slots and
     positions [max_tokens] and free_count_out [1].  If there are too few pages
     (status SA_ERR_CAPACITY) nothing changes hands."""
-    import torch
-    dev = table.device
-    _need(table.dim() == 2, "table must have two axes")
-    B, max_blocks = table.shape
-    num_pages, max_tokens = free_list.numel(), slots.numel()
-    _same(table, torch.int32, (B, max_blocks), "table", dev)
-    _need(not any(t is None for t in (kv_len, q_len, free_list, free_count, new_len, cu_q, slots, positions,
-                                      free_count_out)), "only status may be None")
-    desc = PlanDesc(B, max_blocks, num_pages, max_tokens, int(page), 0)
-    _on(dev, stream, load().sa_cache_plan, _index(kv_len, B, "kv_len", dev), _index(q_len, B, "q_len", dev),
-        ctypes.byref(desc), table.data_ptr(), _index(free_list, num_pages, "free_list", dev),
-        _index(free_count, 1, "free_count", dev), _index(free_count_out, 1, "free_count_out", dev),
-        _index(new_len, B, "new_len", dev), _index(cu_q, B + 1, "cu_q", dev),
-        _index(slots, max_tokens, "slots", dev), _index(positions, max_tokens, "positions", dev),
-        _index(status, 1, "status", dev))
+    code = _binding().cache_plan(kv_len, q_len, table, free_list, free_count, page, new_len, cu_q, slots, positions,
+                                 free_count_out, status, _raw(stream))
+    if code != SA_OK:
+        _check(code)
 
 
 # ---------------------------------------------------------------------------

@@ -606,3 +606,79 @@ def test_a_captured_step_runs_on_new_inputs(torch, sa):
         graph.replay()
         assert torch.equal(a[4], b[4]) and torch.equal(a[1].pages, b[1].pages) and torch.equal(a[0].table, b[0].table)
         assert a[0].kv_len.tolist() == b[0].kv_len.tolist() == [n + i + 1 for n in lens]
+
+
+# ---------------------------------------------------------------------------
+# Many units, and offsets past 32 bits
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("Hq,Hkv,d,window", [(16, 4, 128, 300), (11, 11, 64, 0)])
+def test_window_attn_prefill_of_many_units(torch, sa, Hq, Hkv, d, window):
+    """More units than SMs, so that blocks take a second one, in a padded batch."""
+    c = (2, Hq, Hkv, 1700, 1900, d, "bf16", window, 5, [1700, 1333], [1900, 1334])
+    q, k, v, nq, nk = window_inputs(torch, c)
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:3], 7.0, device="cuda")
+    sa.window_attn(q, k, v, out, lse, window=window, sinks=5, q_len=i32(torch, nq), kv_len=i32(torch, nk), flags=16)
+    o, l, qn, kn, vn = (f64(t) for t in (out, lse, q, k, v))
+    for b in range(2):
+        for h in (0, 1, Hq - 1):
+            kh = h * Hkv // Hq
+            want = S.attention(qn[b, h, :nq[b]], kn[b, kh, :nk[b]], vn[b, kh, :nk[b]], window, 5)
+            check_rows(o[b, h, :nq[b]], l[b, h, :nq[b]], want, d, nk[b], "bf16", 1)
+        assert (o[b, :, nq[b]:] == 7).all() and (l[b, :, nq[b]:] == 7).all()
+    other = torch.empty_like(q)
+    sa.window_attn(q, k, v, other, window=window, sinks=5, q_len=i32(torch, nq), kv_len=i32(torch, nk), flags=8)
+    for b in range(2):
+        # two kernels, each within 2 (2^-8 (1 + 2^-7) sum w |v| + 2^-8 |o|) of the truth, |v| < 6
+        assert (out[b, :, :nq[b]].float() - other[b, :, :nq[b]].float()).abs().max() <= 4 * 2.0 ** -8 * 6
+
+
+def test_offsets_past_32_bits(torch, sa):
+    """K and V of more than 2^31 elements, and a cache of more than 2^32 bytes: the last heads and pages."""
+    B, Hkv, Nk, d = 1, 8, 2 ** 21 + 100, 128
+    k, v = (torch.zeros(B, Hkv, Nk, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    g = torch.Generator(device="cuda").manual_seed(0)
+    tail = 700
+    k[:, :, -tail:].copy_(torch.randn(B, Hkv, tail, d, device="cuda", generator=g))
+    v[:, :, -tail:].copy_(torch.randn(B, Hkv, tail, d, device="cuda", generator=g))
+    for Nq, flags in ((1, 8), (130, 16), (20, 1)):
+        q = torch.randn(B, 2 * Hkv, Nq, d, device="cuda", generator=g).to(torch.bfloat16)
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+        sa.window_attn(q, k, v, out, lse, window=500, sinks=0, flags=flags)
+        for h in (0, 2 * Hkv - 1):
+            want = S.attention(f64(q[0, h]), f64(k[0, h // 2, -tail:]), f64(v[0, h // 2, -tail:]), 500, 0)
+            check_rows(f64(out[0, h]), f64(lse[0, h]), want, d, tail, "bf16", 1)
+    del k, v
+    cache = sa.KV4Cache.allocate(30000, 8, 128, 128)
+    assert cache.pages.numel() > 2 ** 32
+    x = [torch.randn(200, 8, 128, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2)]
+    slots = torch.cat([torch.arange(128) + 29999 * 128, torch.arange(72) + 29123 * 128]).to(torch.int32).cuda()
+    sa.kv4_append(*x, slots, cache)
+    back = [torch.empty_like(t) for t in x]
+    sa.kv4_read(cache, slots, *back)
+    vals = [S.values(*S.quantise(f64(t))) for t in x]
+    for t, want in zip(back, vals):
+        assert np.array_equal(f64(t), S.round_bf16(want))
+    q = torch.randn(1, 8, 128, device="cuda", generator=g).to(torch.bfloat16)
+    out, lse = torch.empty_like(q), torch.empty(1, 8, device="cuda")
+    sa.kv4_attn(q, cache, i32(torch, [[29999, 29123]]), i32(torch, [200]), out, lse, cu_q=i32(torch, [0, 1]))
+    extra = 8 * np.repeat(S.quantise(f64(x[0]))[1], 32, -1)
+    for h in range(8):
+        want = S.attention(f64(q[:, h]), vals[0][:, h], vals[1][:, h], 0, 0, extra=extra[:, h])
+        check_rows(f64(out[:, h]), f64(lse[:, h]), want, 132, 200, "bf16", 2)
+
+
+def test_two_streams_with_workspaces_of_their_own(torch, sa):
+    """Calls that overlap on the GPU do not share anything but their inputs."""
+    c = (4, 8, 2, 1, 3001, 128, "bf16", 0, 0, None, None)
+    q, k, v, _, _ = window_inputs(torch, c)
+    want = torch.empty_like(q)
+    sa.window_attn(q, k, v, want)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = [[torch.zeros_like(q) for _ in range(20)] for _ in streams]
+    for i in range(20):
+        for s, st in enumerate(streams):
+            sa.window_attn(q, k, v, outs[s][i], stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for s in outs for o in s)
