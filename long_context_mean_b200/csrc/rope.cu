@@ -41,10 +41,13 @@ struct RopeArgs {
   uint64_t items_inv;           // ceil(2^40 / items): exact quotients, as numbers times items stay below 2^40
 };
 
+// VEC elements as they lie in memory, and as floats.
 template <typename T, int VEC> struct Pack;
 template <> struct Pack<uint16_t, 8> {
-  static __device__ __forceinline__ void load(const uint16_t* p, float* f) { unpack16(*reinterpret_cast<const uint4*>(p), uint16_t{}, f); }
-  static __device__ __forceinline__ void store(uint16_t* p, const float* f) {
+  using Raw = uint4;
+  static __device__ __forceinline__ Raw load(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
+  static __device__ __forceinline__ void open(const Raw& r, float* f) { unpack16(r, uint16_t{}, f); }
+  static __device__ __forceinline__ Raw close(const float* f) {
     uint4 u;
     uint32_t* w = reinterpret_cast<uint32_t*>(&u);
 #pragma unroll
@@ -52,73 +55,90 @@ template <> struct Pack<uint16_t, 8> {
       __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
       w[i] = *reinterpret_cast<uint32_t*>(&h);
     }
-    *reinterpret_cast<uint4*>(p) = u;
+    return u;
   }
+  static __device__ __forceinline__ void store(uint16_t* p, const Raw& r) { *reinterpret_cast<uint4*>(p) = r; }
 };
 template <> struct Pack<float, 4> {
-  static __device__ __forceinline__ void load(const float* p, float* f) { *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(p); }
-  static __device__ __forceinline__ void store(float* p, const float* f) { *reinterpret_cast<float4*>(p) = *reinterpret_cast<const float4*>(f); }
+  using Raw = float4;
+  static __device__ __forceinline__ Raw load(const float* p) { return *reinterpret_cast<const float4*>(p); }
+  static __device__ __forceinline__ void open(const Raw& r, float* f) { *reinterpret_cast<float4*>(f) = r; }
+  static __device__ __forceinline__ Raw close(const float* f) { return *reinterpret_cast<const float4*>(f); }
+  static __device__ __forceinline__ void store(float* p, const Raw& r) { *reinterpret_cast<float4*>(p) = r; }
 };
-// Any alignment: a pair of elements at a time.
-template <typename T> struct Pack<T, 2> {
+// Any alignment: an element, or a pair, at a time.
+template <typename T, int N> struct Few {
+  struct Raw { T v[N]; };
   static __device__ __forceinline__ float one(uint16_t v) { return bf16_to_f32(v); }
   static __device__ __forceinline__ float one(float v) { return v; }
-  static __device__ __forceinline__ void load(const T* p, float* f) {
-    f[0] = one(p[0]);
-    f[1] = one(p[1]);
+  static __device__ __forceinline__ Raw load(const T* p) {
+    Raw r;
+#pragma unroll
+    for (int i = 0; i < N; ++i) r.v[i] = p[i];
+    return r;
   }
-  static __device__ __forceinline__ void store(T* p, const float* f) {
-    Elem<T>::store(p, f[0]);
-    Elem<T>::store(p + 1, f[1]);
+  static __device__ __forceinline__ void open(const Raw& r, float* f) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = one(r.v[i]);
+  }
+  static __device__ __forceinline__ Raw close(const float* f) {
+    Raw r;
+#pragma unroll
+    for (int i = 0; i < N; ++i) Elem<T>::store(&r.v[i], f[i]);
+    return r;
+  }
+  static __device__ __forceinline__ void store(T* p, const Raw& r) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = r.v[i];
   }
 };
-template <typename T> struct Pack<T, 1> {
-  static __device__ __forceinline__ void load(const T* p, float* f) { f[0] = Pack<T, 2>::one(p[0]); }
-  static __device__ __forceinline__ void store(T* p, const float* f) { Elem<T>::store(p, f[0]); }
-};
+template <typename T> struct Pack<T, 2> : Few<T, 2> {};
+template <typename T> struct Pack<T, 1> : Few<T, 1> {};
 
 // One item: the vector pair (HALF) or vector of a head's rotated channels, or a
 // vector of those that do not turn.
 template <typename T, int VEC, bool HALF>
 struct Item {
   static constexpr int W = VEC < 2 ? 2 : VEC;   // interleaved: whole pairs
-  const T* x;
+  using PV = Pack<T, VEC>;
+  using PW = Pack<T, W>;
   T* y;
   const float2* c;
-  float u[W], v[VEC];
-  int kind;   // 0: nothing, 1: turn, 2: copy
-  __device__ __forceinline__ void load(int half) {
-    if (kind == 0) return;
-    if (HALF || kind == 2) {
-      Pack<T, VEC>::load(x, u);
-      if (kind == 1) Pack<T, VEC>::load(x + half, v);
-    } else {
-      Pack<T, W>::load(x, u);
-    }
+  typename PV::Raw u, v;   // HALF: the pairs' first and second channels; else u: copied channels
+  typename PW::Raw w;      // interleaved pairs
+  int kind;                // 0: nothing, 1: turn, 2: copy
+  __device__ __forceinline__ void load(const T* x, int half) {
+    if (kind == 2 || (HALF && kind == 1)) u = PV::load(x);
+    if (HALF && kind == 1) v = PV::load(x + half);
+    if (!HALF && kind == 1) w = PW::load(x);
   }
   __device__ __forceinline__ void store(int half) {
-    if (kind == 0) return;
-    if (kind == 2) {
-      Pack<T, VEC>::store(y, u);
-    } else if constexpr (HALF) {
+    if (kind == 2) PV::store(y, u);
+    if (kind != 1) return;
+    if constexpr (HALF) {
+      float a[VEC], b[VEC];
+      PV::open(u, a);
+      PV::open(v, b);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float2 w = c[e];
-        const float p = u[e] * w.x - v[e] * w.y, q = v[e] * w.x + u[e] * w.y;
-        u[e] = p;
-        v[e] = q;
+        const float2 t = c[e];
+        const float p = a[e] * t.x - b[e] * t.y, q = b[e] * t.x + a[e] * t.y;
+        a[e] = p;
+        b[e] = q;
       }
-      Pack<T, VEC>::store(y, u);
-      Pack<T, VEC>::store(y + half, v);
+      PV::store(y, PV::close(a));
+      PV::store(y + half, PV::close(b));
     } else {
+      float a[W];
+      PW::open(w, a);
 #pragma unroll
       for (int e = 0; e < W; e += 2) {
-        const float2 w = c[e >> 1];
-        const float p = u[e] * w.x - u[e + 1] * w.y, q = u[e + 1] * w.x + u[e] * w.y;
-        u[e] = p;
-        u[e + 1] = q;
+        const float2 t = c[e >> 1];
+        const float p = a[e] * t.x - a[e + 1] * t.y, q = a[e + 1] * t.x + a[e] * t.y;
+        a[e] = p;
+        a[e + 1] = q;
       }
-      Pack<T, W>::store(y, u);
+      PW::store(y, PW::close(a));
     }
   }
 };
@@ -138,6 +158,33 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     const int64_t* s = z & 1 ? a.ys[z >> 1] : a.xs[z >> 1];
     at[tt][z] = b * s[0] + n * s[1];
   }
+  __syncthreads();
+  const int per_tok = a.heads_all * a.items, all = nt * per_tok;
+  // Item i, its loads under way.
+  auto item = [&](int i) {
+    Item<T, VEC, HALF> m;
+    m.kind = 0;
+    if (i >= all) return m;
+    int tt = 0;
+#pragma unroll
+    for (int x = 1; x < TOK; ++x) tt += i >= x * per_tok;
+    const int r = i - tt * per_tok;
+    int h = (int)(((uint64_t)r * a.items_inv) >> 40);   // r / items
+    const int it = r - h * a.items;
+    const int which = h >= a.heads[0];
+    if (which) h -= a.heads[0];
+    const bool turns = it < a.pair_items;
+    if (!turns && !a.copy[which]) return m;
+    const int ch = turns ? it * (HALF ? VEC : Item<T, VEC, HALF>::W) : a.rot + (it - a.pair_items) * VEC;
+    m.kind = turns ? 1 : 2;
+    m.y = static_cast<T*>(a.y[which]) + at[tt][2 * which + 1] + h * a.ys[which][2] + ch;
+    m.c = cs + tt * half + (HALF ? ch : ch >> 1);
+    m.load(static_cast<const T*>(a.x[which]) + at[tt][2 * which] + h * a.xs[which][2] + ch, half);
+    return m;
+  };
+  // The first item's loads run while the angles are computed, each next one's
+  // while one is turned and stored (items do not overlap, in place either).
+  Item<T, VEC, HALF> m = item(threadIdx.x);
   for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
     const int tt = i / half, f = i - tt * half;
     const int64_t t = t0 + tt, b = t / a.N;
@@ -161,32 +208,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     cs[i] = make_float2(c * a.mag, a.inverse ? -s * a.mag : s * a.mag);
   }
   __syncthreads();
-  const int per_tok = a.heads_all * a.items, all = nt * per_tok;
-  auto item = [&](int i) {
-    Item<T, VEC, HALF> m;
-    m.kind = 0;
-    if (i >= all) return m;
-    int tt = 0;
-#pragma unroll
-    for (int x = 1; x < TOK; ++x) tt += i >= x * per_tok;
-    const int r = i - tt * per_tok;
-    int h = (int)(((uint64_t)r * a.items_inv) >> 40);   // r / items
-    const int it = r - h * a.items;
-    const int which = h >= a.heads[0];
-    if (which) h -= a.heads[0];
-    const bool turns = it < a.pair_items;
-    if (!turns && !a.copy[which]) return m;
-    const int ch = turns ? it * (HALF ? VEC : Item<T, VEC, HALF>::W) : a.rot + (it - a.pair_items) * VEC;
-    m.kind = turns ? 1 : 2;
-    m.x = static_cast<const T*>(a.x[which]) + at[tt][2 * which] + h * a.xs[which][2] + ch;
-    m.y = static_cast<T*>(a.y[which]) + at[tt][2 * which + 1] + h * a.ys[which][2] + ch;
-    m.c = cs + tt * half + (HALF ? ch : ch >> 1);
-    return m;
-  };
-  for (int i = threadIdx.x; i < all; i += kRopeThreads) {
-    Item<T, VEC, HALF> m = item(i);
-    m.load(half);
+  for (int i = threadIdx.x + kRopeThreads; m.kind || i - kRopeThreads < all; i += kRopeThreads) {
+    const Item<T, VEC, HALF> next = item(i);
     m.store(half);
+    m = next;
   }
 }
 
