@@ -488,7 +488,8 @@ typedef struct {
  * padded batch's sequences; rows i >= q_len[b] of out and lse are left as they
  * were.  bf16 with d in {64, 128} runs on the tensor cores; fp32, and other
  * d up to 256 with d * elem_size a multiple of 16, on the CUDA cores.  All
- * tensors 16-byte aligned; lse is nullable; out overlaps no input.  ws:
+ * tensors 16-byte aligned; lse is nullable; out overlaps no input; Nq * Hq
+ * below 2^31.  ws:
  * sa_window_attn_workspace() bytes (0 for an invalid shape), 256-byte aligned;
  * calls that share it must not overlap on the GPU, captured ones included.
  * flags: 0, or one of SA_FLAG_FORCE_SIMT, SA_FLAG_FORCE_DECODE,
@@ -539,8 +540,12 @@ sa_status sa_kv4_read(const void* cache, const sa_kv4_desc* desc, const int32_t*
  * cu_q[B] are left as they were.  table: device int32 [B][max_blocks], block i
  * of a sequence holds its keys i * page ..; entries that no visible key needs
  * may hold anything.  kv_len: device int32 [B], the new tokens included.
- * window and sinks as above.  ws: sa_kv4_attn_workspace() bytes, 256-byte
- * aligned, not to be shared by calls that overlap on the GPU. */
+ * window and sinks as above.  Few new tokens a sequence are what it is made
+ * for: every 16 rows (tokens times query heads of a kv head) read the cache
+ * once.  Queries above 2^100 in magnitude, and values of V above 2^50, overflow;
+ * weights times scales of V below 2^-57 are lost.  T * Hq below 2^31.  ws:
+ * sa_kv4_attn_workspace() bytes, 256-byte aligned, not to be shared by calls
+ * that overlap on the GPU. */
 size_t sa_kv4_attn_workspace(const sa_kv4_desc* desc, int64_t Hq);
 sa_status sa_kv4_attn(const void* q, int64_t T, int64_t Hq, const int64_t q_strides[2], const int32_t* cu_q,
                       int64_t B, const void* cache, const sa_kv4_desc* desc, const int32_t* table,

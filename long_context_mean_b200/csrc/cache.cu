@@ -142,19 +142,41 @@ __global__ void __launch_bounds__(256) kv4_rows_kernel(const __grid_constant__ R
   const Place<G> at(live ? slot : 0, a.lg_page, a.H, h, cc);
   constexpr int NEXT = 16 * G;   // V's next 4 channels
   uint8_t* p = a.cache + at.base;
+  const uint8_t* p_in = p;
   // The first half warp moves the pair's first 4 channels of V, the second the next 4.
   const int at_v = pair && half ? at.v - 2 + NEXT : at.v;
   const uint16_t *k_in = a.k + t * a.ks[0] + h * a.ks[1] + cc * 8, *v_in = a.v + t * a.vs[0] + h * a.vs[1] + cc * 8;
   uint16_t *k_out = a.ko + t * a.ks[0] + h * a.ks[1] + cc * 8, *v_out = a.vo + t * a.vs[0] + h * a.vs[1] + cc * 8;
+  // Each block's loads run while the one before is worked on.
+  uint4 k2 = make_uint4(0, 0, 0, 0), v2 = k2;   // WRITE
+  uint32_t kc2 = 0, mine2 = 0;                  // read
+  uint16_t sk2 = 0, sv2r = 0;
+  auto fetch = [&](int head) {
+    if (!(live && head < a.H)) return;
+    if constexpr (WRITE) {
+      k2 = a.wide ? __ldg(reinterpret_cast<const uint4*>(k_in)) : load8(k_in);
+      v2 = a.wide ? __ldg(reinterpret_cast<const uint4*>(v_in)) : load8(v_in);
+      k_in += HEADS * a.ks[1];
+      v_in += HEADS * a.vs[1];
+    } else {
+      kc2 = __ldg(reinterpret_cast<const uint32_t*>(p_in + at.k));
+      sk2 = __ldg(reinterpret_cast<const uint16_t*>(p_in + at.ks));
+      sv2r = __ldg(reinterpret_cast<const uint16_t*>(p_in + at.vs));
+      if (pair)
+        mine2 = __ldg(reinterpret_cast<const uint32_t*>(p_in + at_v));
+      else
+        mine2 = __ldg(reinterpret_cast<const uint16_t*>(p_in + at.v)) |
+                (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p_in + at.v + NEXT)) << 16;
+      p_in += (int64_t)HEADS * (576 * G) << (a.lg_page - 4);
+    }
+  };
+  fetch(h);
 #pragma unroll 2
   for (int i = 0; i < a.each; ++i) {
     const bool on = live && h < a.H;   // a group's 4 lanes, and a pair's two, agree
     if constexpr (WRITE) {
-      uint4 k = make_uint4(0, 0, 0, 0), v = k;
-      if (on) {
-        k = a.wide ? __ldg(reinterpret_cast<const uint4*>(k_in)) : load8(k_in);
-        v = a.wide ? __ldg(reinterpret_cast<const uint4*>(v_in)) : load8(v_in);
-      }
+      const uint4 k = k2, v = v2;
+      if (i + 1 < a.each) fetch(h + HEADS);
       uint32_t m = abs_max8(k), n = abs_max8(v);
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) {
@@ -177,21 +199,11 @@ __global__ void __launch_bounds__(256) kv4_rows_kernel(const __grid_constant__ R
           if ((cc & 3) == 0) *reinterpret_cast<uint16_t*>(p + at.vs) = sv;
         }
       }
-      k_in += HEADS * a.ks[1];
-      v_in += HEADS * a.vs[1];
+      p += (int64_t)HEADS * (576 * G) << (a.lg_page - 4);
     } else {
-      uint32_t kc = 0, mine = 0;
-      uint16_t sk = 0, sv = 0;
-      if (on) {
-        kc = __ldg(reinterpret_cast<const uint32_t*>(p + at.k));
-        sk = __ldg(reinterpret_cast<const uint16_t*>(p + at.ks));
-        sv = __ldg(reinterpret_cast<const uint16_t*>(p + at.vs));
-        if (pair)
-          mine = __ldg(reinterpret_cast<const uint32_t*>(p + at_v));
-        else
-          mine = __ldg(reinterpret_cast<const uint16_t*>(p + at.v)) |
-                 (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p + at.v + NEXT)) << 16;
-      }
+      const uint32_t kc = kc2, mine = mine2;
+      const uint16_t sk = sk2, sv = sv2r;
+      if (i + 1 < a.each) fetch(h + HEADS);
       const uint32_t got = __shfl_xor_sync(0xffffffffu, half ? mine & 0xFFFFu : mine >> 16, 16);
       if (on) {
         const uint32_t vc = !pair ? mine : half ? got | (mine & 0xFFFF0000u) : (mine & 0xFFFFu) | got << 16;
@@ -202,7 +214,6 @@ __global__ void __launch_bounds__(256) kv4_rows_kernel(const __grid_constant__ R
       v_out += HEADS * a.vs[1];
     }
     h += HEADS;
-    p += (int64_t)HEADS * (576 * G) << (a.lg_page - 4);
   }
 }
 
@@ -216,7 +227,7 @@ template <bool WRITE>
 sa_status launch_rows(RowArgs& a, const sa_kv4_desc& d, cudaStream_t st) {
   // Once two warps an SM sub-partition are there, a warp walks several heads.
   const int64_t blocks = ceil_div(d.Hkv * (d.d / 8), 16), pairs = ceil_div(a.T, 2);
-  a.each = (int32_t)max64(1, min64(min64(blocks, 8), pairs * blocks / (148 * 8)));
+  a.each = (int32_t)max64(1, min64(min64(blocks, 4), pairs * blocks / (148 * 8)));
   const int64_t ctas = ceil_div(pairs * ceil_div(blocks, a.each), 8);
   if (ctas == 0) return SA_OK;
   if (ctas > 2147483647 / 8) return set_error(SA_ERR_UNSUPPORTED, "too many rows");

@@ -25,7 +25,7 @@ sa_status check_window_shape(const sa_window_shape* s) {
     return set_error(SA_ERR_INVALID_ARG, "shape sizes must be positive");
   if (s->Hq % s->Hkv != 0) return set_error(SA_ERR_INVALID_ARG, "Hq must be a multiple of Hkv");
   if (s->dtype != SA_BF16 && s->dtype != SA_FP32) return set_error(SA_ERR_INVALID_ARG, "unknown dtype");
-  if (s->Nq > kInt32 / 2 || s->Nk > kInt32 / 2 || s->B > kInt32 / 2 || s->Hq > 65535)
+  if (s->Nq > kInt32 / 2 || s->Nk > kInt32 / 2 || s->B > kInt32 / 2 || s->Hq > 65535 || s->Nq * s->Hq > kInt32)
     return set_error(SA_ERR_UNSUPPORTED, "sizes too large");
   const int es = s->dtype == SA_BF16 ? 2 : 4;
   if (s->d > 256 || s->d * es % 16 != 0)
@@ -179,7 +179,7 @@ sa_status sa_kv4_attn(const void* q, int64_t T, int64_t Hq, const int64_t q_stri
   if (sa_status e = check_window(window, sinks, scale)) return e;
   if (T < 0 || B < 0 || max_blocks < 0 || Hq <= 0) return set_error(SA_ERR_INVALID_ARG, "negative size");
   if (Hq % desc->Hkv != 0) return set_error(SA_ERR_INVALID_ARG, "Hq must be a multiple of Hkv");
-  if (T > kInt32 / 2 || B > kInt32 / 2 || Hq > 65535 || max_blocks > kInt32 / 2 / desc->page)
+  if (T > kInt32 / 2 || B > kInt32 / 2 || Hq > 65535 || T * Hq > kInt32 || max_blocks > kInt32 / 2 / desc->page)
     return set_error(SA_ERR_UNSUPPORTED, "sizes too large");
   if (T == 0 || B == 0) return SA_OK;   // no row
   if (max_blocks == 0) return set_error(SA_ERR_INVALID_ARG, "max_blocks must be positive");

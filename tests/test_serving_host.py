@@ -45,7 +45,8 @@ def window_code(lib, shape=(2, 4, 2, 5, 70, 128, sa.SA_BF16), window=8, sinks=1,
 @pytest.mark.parametrize("kw,code", [
     (dict(shape=(0, 4, 2, 5, 70, 128, 0)), BAD), (dict(shape=(2, 4, 3, 5, 70, 128, 0)), BAD),
     (dict(shape=(2, 4, 2, 5, 70, 128, 7)), BAD), (dict(shape=(2, 4, 2, 5, 70, 36, 0)), UNSUP),
-    (dict(shape=(2, 4, 2, 5, 70, 264, 1)), UNSUP), (dict(shape=(1, 4, 2, 1 << 40, 70, 128, 0)), UNSUP),
+    (dict(shape=(2, 4, 2, 5, 70, 264, 1)), UNSUP), (dict(shape=(1, 64, 2, 1 << 26, 70, 128, 0)), UNSUP),
+    (dict(shape=(1, 4, 2, 1 << 40, 70, 128, 0)), UNSUP),
     (dict(window=-1), BAD), (dict(sinks=-1), BAD), (dict(window=1 << 33), UNSUP), (dict(scale=-1.0), BAD),
     (dict(scale=math.nan), BAD), (dict(scale=math.inf), BAD), (dict(q=NULL), BAD), (dict(out=NULL), BAD),
     (dict(q=ctypes.c_void_p(0x100000008)), BAD), (dict(out=at(0)), BAD), (dict(out=at(64)), BAD),
@@ -87,7 +88,7 @@ def test_kv4_row_refusals(lib):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(T=-1), BAD), (dict(Hq=3), BAD), (dict(Hq=0), BAD), (dict(mb=0), BAD), (dict(mb=1 << 40), UNSUP),
+    (dict(T=-1), BAD), (dict(T=1 << 29, Hq=8), UNSUP), (dict(Hq=3), BAD), (dict(Hq=0), BAD), (dict(mb=0), BAD), (dict(mb=1 << 40), UNSUP),
     (dict(q=NULL), BAD), (dict(cu=NULL), BAD), (dict(table=NULL), BAD), (dict(kv_len=NULL), BAD),
     (dict(qs=(516, 128)), BAD), (dict(q=ctypes.c_void_p(0x100000008)), BAD), (dict(out=at(0)), BAD),
     (dict(out=at(64)), BAD), (dict(lse=at(128)), BAD), (dict(ws=NULL), WS), (dict(n=64), WS),
