@@ -52,7 +52,7 @@ constexpr float kRescale = 8.f;
 // What a worker leaves for join_kernel.
 struct Piece {
   int32_t last;          // the piece that ends the unit which begins in this one and goes on past it; 0: none
-  int32_t b, row0, kvh;  // that unit
+  int32_t b, row0, kvh, n_q, q0;  // that unit, as join_kernel needs it
 };
 
 struct DecodeArgs {
@@ -785,6 +785,8 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
       piece.b = u.b;
       piece.row0 = u.row0;
       piece.kvh = u.kvh;
+      piece.n_q = u.n_q;
+      piece.q0 = u.q0;
     }
     // The rings are filled next by the async proxy, after these generic accesses.
     if (F::kBulk) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -800,14 +802,15 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
 // as a dependent of decode_kernel: it waits for that grid's writes.
 template <class F, int D, int NQ>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ DecodeArgs a) {
-  constexpr int ROWS = 8 * NQ, C8 = D / 8, BATCH = 4;
+  constexpr int ROWS = 8 * NQ, C8 = D / 8, BATCH = 6;
   __shared__ float part[kJoinThreads][11];   // m, l and 8 sums of a thread
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Piece p = a.pieces[blockIdx.x];
   if (p.last == 0) return;
-  Unit u;
-  int rt, tl;
-  sequence<F::TOK, ROWS>(a, p.b, u, rt, tl);
+  Unit u{};
+  u.b = p.b;
+  u.q0 = p.q0;
+  u.n_q = p.n_q;
   u.row0 = p.row0;
   u.kvh = p.kvh;
   const int rows = min(ROWS, u.n_q * a.group - u.row0), items = rows * C8;

@@ -16,7 +16,7 @@
 // keys interleaved so that a warp's 4 row groups and 8 key groups each read one
 // wavefront of shared memory: 8 wavefronts feed 64 multiply-adds a lane.  K and then
 // V of a tile go through one buffer a warp; 16 warps an SM (d = 64) cover its
-// latency.  2 x 1000 rows, 8 heads, d = 64, window 256: 63 us (64 x 64 tiles of a
+// latency.  2 x 1000 rows, 8 heads, d = 64, window 256: 55 us (64 x 64 tiles of a
 // block, and 32 x 32 tiles with 8 rows a lane and two buffers, 80: 8 warps an SM
 // leave the pipes idle half the time).
 #include "sa_internal.cuh"
@@ -69,37 +69,59 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// 16 bytes of a row to shared memory as floats (zeros where !on), from `at` to `to`:
+// fp32 by an asynchronous copy, which the caller waits for.
+template <typename T>
+__device__ __forceinline__ void move16(uint32_t to, const T* at, bool on) {
+  if constexpr (sizeof(T) == 4) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(at), "r"(on ? 16 : 0) : "memory");
+  } else {
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (on) w = __ldg(reinterpret_cast<const uint4*>(at));
+    float f[8];
+    unpack16(w, T{}, f);
+#pragma unroll
+    for (int e = 0; e < 8; e += 4)
+      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to + 4 * e), "f"(f[e]), "f"(f[e + 1]), "f"(f[e + 2]),
+                   "f"(f[e + 3])
+                   : "memory");
+  }
+}
 // Rows r0 .. r0 + n - 1 of a [..][d] array as floats to shared memory, row stride
 // d + 4 (16-byte reads of neighbouring rows then meet no bank twice), by threads i0,
-// i0 + step, ..; rows that live() leaves out come as zeros.  fp32 goes by
-// asynchronous copies, which the caller waits for.
+// i0 + step, ..; rows that live() leaves out (of those relative to r0) come as zeros.
+// all: none is left out.  Where whole rows make a step, a thread keeps its
+// column and nothing is computed but two addresses: the general walk took a
+// third of the kernel's instructions.
 template <typename T, class Live>
-__device__ __forceinline__ void load_rows(float* dst, const T* src, int64_t r0, int n, int d, int i0, int step, Live live) {
+__device__ __forceinline__ void load_rows(float* dst, const T* src, int64_t r0, int n, int d, int i0, int step, bool all,
+                                          Live live) {
   constexpr int V = 16 / sizeof(T);
   const int per = d / V, dr = step / per, dc = step - dr * per;
   int r = i0 / per, c = i0 - r * per;
   const T* at = src + r0 * d + (int64_t)i0 * V;   // (rows follow one another)
   uint32_t to = (uint32_t)__cvta_generic_to_shared(dst + r * (d + 4)) + c * V * 4;
-  while (r < n) {
-    const bool on = live(r0 + r);
-    if constexpr (sizeof(T) == 4) {
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(on ? at : src), "r"(on ? 16 : 0) : "memory");
-    } else {
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (on) w = __ldg(reinterpret_cast<const uint4*>(at));
-      float f[V];
-      unpack16(w, T{}, f);
-#pragma unroll
-      for (int e = 0; e < V; e += 4) *reinterpret_cast<float4*>(dst + r * (d + 4) + c * V + e) = *reinterpret_cast<float4*>(f + e);
+  const uint32_t dto = (step * V + dr * 4) * 4;   // 4 floats of padding a row
+  if (all && dc == 0) {
+#pragma unroll 4
+    for (; r < n; r += dr) {
+      move16<T>(to, at, true);
+      at += step * V;
+      to += dto;
     }
-    at += step * V;
-    to += (step * V + dr * 4) * 4;   // 4 floats of padding a row
-    r += dr;
-    c += dc;
-    if (c >= per) {
-      c -= per;
-      ++r;
-      to += 16;
+  } else {
+    for (; r < n;) {
+      const bool on = live(r);
+      move16<T>(to, on ? at : src, on);
+      at += step * V;
+      to += dto;
+      r += dr;
+      c += dc;
+      if (c >= per) {
+        c -= per;
+        ++r;
+        to += 16;
+      }
     }
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -142,10 +164,15 @@ __global__ void __launch_bounds__(32 * W, (CW <= 2 ? 16 : CW == 4 ? 12 : 8) / W)
   const int64_t t_lo = max64(sink_tiles, lo / kKeys);
   const int tiles = (int)(sink_tiles + max64(0, ceil_div_d(hi, kKeys) - t_lo));
   auto key0 = [&](int t) { return (t < sink_tiles ? t : t_lo + (t - sink_tiles)) * kKeys; };
-  auto live = [&](int64_t j) { return j < hi && (j >= lo || j < n_sink); };
+  // The tile's rows of K or V, zeros for keys that no row sees.
+  auto load_tile = [&](const T* src, int64_t k0) {
+    const int a1 = (int)min64(n_sink - k0, kKeys), b0 = (int)min64(lo - k0, kKeys), b1 = (int)min64(hi - k0, kKeys);
+    load_rows<T>(ks, src, k0, kKeys, d, lane, 32, b1 == kKeys && (b0 <= 0 || a1 == kKeys),
+                 [&](int r) { return r < b1 && (r >= b0 || r < a1); });
+  };
 
-  load_rows<T>(qs, q, row0, ROWS, d, threadIdx.x, kThreads, [&](int64_t r) { return r < n_q; });
-  if (warp < tiles) load_rows<T>(ks, k, key0(warp), kKeys, d, lane, 32, live);
+  load_rows<T>(qs, q, row0, ROWS, d, threadIdx.x, kThreads, row0 + ROWS <= n_q, [&](int r) { return row0 + r < n_q; });
+  if (warp < tiles) load_tile(k, key0(warp));
   wait_rows();
   __syncthreads();   // (Q; the only one before the join)
   uint64_t o[RT][2 * CW];   // channel pairs
@@ -181,7 +208,7 @@ __global__ void __launch_bounds__(32 * W, (CW <= 2 ? 16 : CW == 4 ? 12 : 8) / W)
       }
     }
     __syncwarp();
-    load_rows<T>(ks, v, k0, kKeys, d, lane, 32, live);
+    load_tile(v, k0);
     const bool whole = k0 + kKeys - 1 <= first && (a.window == 0 || last - k0 < a.window || k0 + kKeys <= a.sinks);
     // (positions relative to the tile; a valid row's is below n_k)
     const int p0 = (int)(first - k0) + ty, c_s = (int)min64(a.sinks - k0, kKeys);
@@ -239,7 +266,7 @@ __global__ void __launch_bounds__(32 * W, (CW <= 2 ? 16 : CW == 4 ? 12 : 8) / W)
       }
     }
     __syncwarp();
-    if (t + W < tiles) load_rows<T>(ks, k, key0(t + W), kKeys, d, lane, 32, live);
+    if (t + W < tiles) load_tile(k, key0(t + W));
   }
   // Each warp's part over its K and P: O [ROWS][d + 4] and, behind it, m and l.
   __syncwarp();
