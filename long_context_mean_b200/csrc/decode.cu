@@ -249,7 +249,7 @@ struct Kv4 {
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const int x = min(127, 141 - (int)(top >> 7));
     const float up = __uint_as_float((uint32_t)(127 + x) << 23);
-    const float unit = scale_log2 * 0x1p24f / up;
+    const float unit = fmaxf(scale_log2 * 0x1p24f / up, 1.17549435e-38f);   // (0 times a masked -inf would be NaN)
 #pragma unroll
     for (int c = 0; c < 2; ++c) q.unit[c] = __shfl_sync(0xffffffffu, unit, (2 * q4 + c) * 4);
     float lead[2] = {0.f, 0.f};   // the sums of groups 2 (q4 % 2), + 1

@@ -474,7 +474,9 @@ def _call_workspace(nbytes, t, name, stream):
     _need(t.is_cuda, f"{name} must be on a CUDA device")
     ws = workspace(nbytes, t.device)
     if stream is not None:
-        ws.record_stream(stream)     # it stays allocated until that stream has used it
+        import torch
+        if not torch.cuda.is_current_stream_capturing():
+            ws.record_stream(stream)     # it stays allocated until that stream has used it
     return ws
 
 

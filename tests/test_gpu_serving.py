@@ -12,7 +12,10 @@ output's rounding u |o|, and sums of n terms n 2^-24.  The cache's K enters as
 sum of a 32-channel group is then at most sum |q_c| (|code_c| + 8) times its scale,
 so e counts |k_c| + 8 s_c in the place of |k_c|, with 3 x 32 products, 32 terms of the
 sum of q, the offset, the scale and the 4 groups: below (d + 8) roundings of 2^-24 for
-d = 128 and below 140 for either d.
+d = 128 and below 140 for either d.  Its V enters as (code + 8) too, with 8 sum w taken off
+by the next product, so that O's partial sums reach sum w s (|code| + 8): each of the two
+products of 16 tokens, and each joining of parts, rounds (or cuts) that by 2^-23 at most,
+n / 8 + 16 of them.
 """
 
 import math
@@ -47,12 +50,13 @@ def i32(torch, x):
 
 def check_rows(out, lse, want, d, n, dtype, roundings):
     """One head's rows against attention()'s result; roundings: bf16 roundings of a weight."""
-    o, l, absv, size = want
+    o, l, absv, size, sums = want
     assert np.isfinite(out).all()
     e = (d + 8) * 2.0 ** -24 * size[:, None]
     rel = 2 * e + 2.0 ** -21 + n * 2.0 ** -23 + roundings * 2.0 ** -8 * (1 + 2.0 ** -7)
     last = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -23
-    assert (np.abs(out - o) <= last * (np.abs(o) + rel * absv) + rel * absv + 1e-38).all(), np.abs(out - o).max()
+    off = rel * absv + (n / 8 + 16) * 2.0 ** -23 * sums
+    assert (np.abs(out - o) <= last * (np.abs(o) + off) + off + 1e-38).all(), np.abs(out - o).max()
     none = np.isinf(l)
     assert np.array_equal(np.isneginf(lse), none) and (out[none] == 0).all()
     ok = ~none
@@ -300,7 +304,7 @@ def paged(torch, sa, c, seed=0):
         k, v = (torch.randn(n, Hkv, d, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
         slots = torch.tensor([order[used + i // page] * page + i % page for i in range(n)], dtype=torch.int32, device="cuda")
         sa.kv4_append(k, v, slots, cache)
-        vals.append([S.values(*S.quantise(f64(x))) for x in (k, v)] + [8 * np.repeat(S.quantise(f64(k))[1], 32, -1)])
+        vals.append([S.values(*S.quantise(f64(x))) for x in (k, v)] + [8 * np.repeat(S.quantise(f64(x))[1], 32, -1) for x in (k, v)])
         used += blocks[b]
     q = (torch.randn(sum(nq) + 2, Hq, d, device="cuda", generator=g) * 1.5).to(torch.bfloat16)
     cu = i32(torch, [sum(nq[:i]) for i in range(len(nq) + 1)])
@@ -325,8 +329,8 @@ def test_kv4_attn(torch, sa, c):
     o, l, qn, at = f64(out), f64(lse), f64(q), 0
     for b, (n, k) in enumerate(zip(nq, nk)):
         for h in range(Hq):
-            kh, vh, extra = (x[:, h * Hkv // Hq] for x in vals[b])
-            want = S.attention(qn[at:at + n, h], kh, vh, window, sinks, extra=extra)
+            kh, vh, ek, ev = (x[:, h * Hkv // Hq] for x in vals[b])
+            want = S.attention(qn[at:at + n, h], kh, vh, window, sinks, extra=ek, extra_v=ev)
             check_rows(o[at:at + n, h], l[at:at + n, h], want, 132, k, "bf16", 2)
         at += n
     assert (o[at:] == 7).all() and (l[at:] == 7).all()
@@ -534,7 +538,7 @@ def test_steps_together(torch, sa):
     cache.pages.fill_(255)
     rope = sa.Rope(64, layout="half")
     ws = sa.workspace(sa.kv4_attn_workspace(cache, Hq), "cuda")
-    past = [[np.zeros((0, Hkv, d))] * 3 for _ in range(B)]
+    past = [[np.zeros((0, Hkv, d))] * 4 for _ in range(B)]
     q_in, k_in = (torch.zeros(140, h, d, dtype=torch.bfloat16, device="cuda") for h in (Hq, Hkv))
     v_in, out = torch.zeros_like(k_in), torch.zeros_like(q_in)
     lse = torch.zeros(140, Hq, device="cuda")
@@ -555,10 +559,10 @@ def test_steps_together(torch, sa):
             rows = slice(at, at + n)
             for i, x in enumerate((kr, v_in)):
                 past[b][i] = np.concatenate([past[b][i], S.values(*S.quantise(f64(x[rows])))])
-            past[b][2] = np.concatenate([past[b][2], 8 * np.repeat(S.quantise(f64(kr[rows]))[1], 32, -1)])
+                past[b][2 + i] = np.concatenate([past[b][2 + i], 8 * np.repeat(S.quantise(f64(x[rows]))[1], 32, -1)])
             for h in range(Hq):
-                kh, vh, extra = (x[:, h * Hkv // Hq] for x in past[b])
-                want = S.attention(qn[rows, h], kh, vh, window, sinks, extra=extra)
+                kh, vh, ek, ev = (x[:, h * Hkv // Hq] for x in past[b])
+                want = S.attention(qn[rows, h], kh, vh, window, sinks, extra=ek, extra_v=ev)
                 check_rows(o[rows, h], l[rows, h], want, 132, len(past[b][0]), "bf16", 2)
             at += n
         k.turn()
@@ -662,9 +666,9 @@ def test_offsets_past_32_bits(torch, sa):
     q = torch.randn(1, 8, 128, device="cuda", generator=g).to(torch.bfloat16)
     out, lse = torch.empty_like(q), torch.empty(1, 8, device="cuda")
     sa.kv4_attn(q, cache, i32(torch, [[29999, 29123]]), i32(torch, [200]), out, lse, cu_q=i32(torch, [0, 1]))
-    extra = 8 * np.repeat(S.quantise(f64(x[0]))[1], 32, -1)
+    ek, ev = (8 * np.repeat(S.quantise(f64(t))[1], 32, -1) for t in x)
     for h in range(8):
-        want = S.attention(f64(q[:, h]), vals[0][:, h], vals[1][:, h], 0, 0, extra=extra[:, h])
+        want = S.attention(f64(q[:, h]), vals[0][:, h], vals[1][:, h], 0, 0, extra=ek[:, h], extra_v=ev[:, h])
         check_rows(f64(out[:, h]), f64(lse[:, h]), want, 132, 200, "bf16", 2)
 
 
@@ -682,3 +686,71 @@ def test_two_streams_with_workspaces_of_their_own(torch, sa):
             sa.window_attn(q, k, v, outs[s][i], stream=st)
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for s in outs for o in s)
+
+
+# ---------------------------------------------------------------------------
+# Refusals of the binding, and the ends of the queries' range
+# ---------------------------------------------------------------------------
+
+def test_the_binding_refuses(torch, sa):
+    z = lambda *n, dt=torch.bfloat16, dev="cuda": torch.zeros(*n, dtype=dt, device=dev)   # noqa: E731
+    q, k = z(2, 4, 3, 64), z(2, 2, 9, 64)
+    i2 = i32(torch, [3, 3])
+
+    def window(q=q, k=k, v=k, out=None, **kw):
+        sa.window_attn(q, k, v, torch.zeros_like(q) if out is None else out, **kw)
+    window()
+    for kw, what in ((dict(k=k.float()), "k must be a"), (dict(k=k.cpu(), v=k.cpu()), "same CUDA device"), (dict(v=z(2, 2, 8, 64)), "shape"),
+                     (dict(out=z(2, 4, 3, 128)), "out must have shape"), (dict(q=q.transpose(1, 2)), "contiguous|shape"),
+                     (dict(q_len=i2.long()), "q_len"), (dict(q_len=i2[:1]), "q_len"), (dict(kv_len=i2.cpu()), "kv_len"),
+                     (dict(lse=z(2, 4, 3)), "lse"), (dict(ws=z(512, dt=torch.uint8, dev="cpu")), "ws"),
+                     (dict(q=q.half(), k=k.half(), v=k.half(), out=q.half()), "unsupported dtype")):
+        with pytest.raises(ValueError, match=what):
+            window(**kw)
+    with pytest.raises(sa.SAError, match="WORKSPACE"):
+        window(ws=z(256, dt=torch.uint8))
+    with pytest.raises(sa.SAError, match="overlap"):
+        window(out=q)
+    with pytest.raises(sa.SAError, match="UNSUPPORTED"):
+        sa.window_attn(*(z(1, 1, 2, 20) for _ in range(4)))       # 40 bytes a row
+    cache = sa.KV4Cache.allocate(2, 2, 16, 64)
+    row, slots = z(5, 2, 64), i32(torch, range(5))
+    for args, what in (((row[:4], row, slots), "v must have shape"), ((row, row, slots[:4]), "slots"),
+                       ((row.float(), row, slots), "k must be a"), ((z(5, 64, 2).transpose(1, 2), row, slots), "channels"),
+                       ((row.cpu(), row, slots), "same CUDA device")):
+        with pytest.raises(ValueError, match=what):
+            sa.kv4_append(*args, cache)
+    with pytest.raises(ValueError, match="k must"):
+        sa.kv4_read(cache, slots, row[:, :1], row)
+    with pytest.raises(sa.SAError, match="8-byte|strides"):
+        sa.kv4_append(z(5, 2, 65)[..., 1:], row, slots, cache)
+    with pytest.raises(ValueError, match="cu_q"):
+        sa.kv4_attn(z(1, 2, 64), cache, i32(torch, [[0]]), i32(torch, [4]), z(1, 2, 64), cu_q=i32(torch, [0]))
+    r = sa.Rope(64)
+    for args, what in (((i32(torch, range(4)), row, row), "pos"), ((i32(torch, range(5)), row, row[:, :1]), "q_out"),
+                       ((i32(torch, range(5)), row, row, row), "k and k_out")):
+        with pytest.raises(ValueError, match=what):
+            sa.rope(r, *args)
+    with pytest.raises(sa.SAError, match="rot_dim"):
+        sa.rope(sa.Rope(128), i32(torch, range(5)), row, torch.zeros_like(row))
+    b = Book(torch, sa, 3, 4, 5, 16, 9)
+    b.cu = b.cu[:3]
+    with pytest.raises(ValueError, match="cu_q"):
+        b.step([1, 1, 1])
+
+
+@pytest.mark.parametrize("size,scale", [(0.0, 0.0), (0.0, 1e-30), (1e-36, 0.0), (1e30, 1e-30)])
+def test_kv4_attn_queries_of_any_size(torch, sa, size, scale):
+    """Zero, tiny and huge queries: the power of two that fp16 takes them at follows their size."""
+    c = (8, 2, 128, 16, [100, 40], [1, 2], 30, 2)
+    q, cache, table, kv_len, cu, vals = paged(torch, sa, c)
+    q = (q.float() * size).to(torch.bfloat16)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    sa.kv4_attn(q, cache, table.cuda(), kv_len, out, lse, cu_q=cu, window=30, sinks=2, scale=scale)
+    o, l, qn, at = f64(out), f64(lse), f64(q), 0
+    for b, (n, k) in enumerate(zip(c[5], c[4])):
+        for h in range(8):
+            kh, vh, ek, ev = (x[:, h // 4] for x in vals[b])
+            want = S.attention(qn[at:at + n, h], kh, vh, 30, 2, scale, extra=ek, extra_v=ev)
+            check_rows(o[at:at + n, h], l[at:at + n, h], want, 132, k, "bf16", 2)
+        at += n
