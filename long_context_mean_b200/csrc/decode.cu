@@ -23,10 +23,10 @@
 //    memory: the widened codes would have to be written there, 4 times the bytes
 //    that arrive.)
 //  * KV4, bound by the instructions that widen the codes: a nibble under a mask is
-//    an fp16 (K) or bf16 (V) number already (below), five instructions for 8 codes,
-//    and products with constants take the offset 8 off; K's scales multiply the
+//    an fp16 (K) or bf16 (V) number already (below), five instructions for 8 codes;
+//    a product takes K's offset 8 off, a subtraction V's; K's scales multiply the
 //    32-channel partial scores in fp32, V's scales multiply P.  16 sequences of 8,000
-//    to 30,000 tokens, 312 MB: 75 us (4.2 TB/s); nibbles widened to bf16 integers by
+//    to 30,000 tokens, 312 MB: 68 us (4.6 TB/s); nibbles widened to bf16 integers by
 //    shift, AND-OR and subtraction took 108, 8-bit operands (converted back to
 //    fp16 by the compiler) 165.
 // Rounding: P (and P times the V scale) is rounded to bf16 for the second
@@ -158,6 +158,10 @@ __device__ __forceinline__ uint32_t pack2h(float lo, float hi) {
   __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
 }
+__device__ __forceinline__ uint32_t sub2bf(uint32_t a, uint32_t b) {
+  __nv_bfloat162 r = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
 __device__ __forceinline__ uint32_t mul2bf(uint32_t a, uint32_t b) {
   __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
   return *reinterpret_cast<uint32_t*>(&r);
@@ -213,8 +217,8 @@ __device__ __forceinline__ int tile_at(const Unit& u, int i) { return i < u.sink
 template <int D>
 struct Kv4 {
   static constexpr int G = D / 32, SUBS = 4, TOK = 16 * SUBS, SUB_BYTES = 576 * G, STAGE = SUBS * SUB_BYTES;
-  // 64 tokens a tile, two stages a warp, 12 warps an SM: 75 us for 312 MB, with 32
-  // tokens and three stages 83 (12 warps) and 87 (16, whose 128 registers spill).
+  // 64 tokens a tile, two stages a warp, 12 warps an SM; with 32 tokens and three
+  // stages a tenth slower, with 16 warps more (their 128 registers spill).
   static constexpr int STAGES = 2, TILES = D / 16;
   static constexpr int CTAS = 3;
   // What a unit costs beside its tiles, in tiles (its lengths, queries and output
@@ -352,9 +356,9 @@ struct Kv4 {
   }
   // A code + 8 in the low bits of a bf16 is (code + 8) 2^-133, one nibble
   // higher 16 times that (bf16's subnormals and first binade are linear): masks
-  // again, and a product with a constant - 8 takes the offset off at once, so that
-  // the sums stay as small as without it.  P comes times 2^kShift, which keeps
-  // the products far from fp32's smallest numbers.
+  // again, and an exact subtraction of the offset (by products with a constant - 8
+  // instead: 72 us where this takes 68, and sums of 8 w that cancel).  P comes times
+  // 2^kShift, which keeps the products far from fp32's smallest numbers.
   static constexpr float kShift = 64.f;
   static __device__ __forceinline__ float gain(int half) { return half ? 0x1p65f : 0x1p69f; }   // 2^(133 - kShift), / 16
   // p: P as B operands (tokens 2 (lane % 4), + 1 and + 8, + 9).  keep: one bit per
@@ -380,15 +384,15 @@ struct Kv4 {
     }
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      constexpr uint32_t L = 0x000F000Fu, H = 0x00F000F0u, OFF = 0x80088008u, OFF16 = 0x80808080u;
+      constexpr uint32_t L = 0x000F000Fu, H = 0x00F000F0u, L8 = 0x00080008u, H8 = 0x00800080u;
       const uint32_t y0 = v0[g] >> 8, y1 = v1[g] >> 8;
+      const uint32_t a0 = sub2bf(v0[g] & L, L8), a1 = sub2bf(v0[g] & H, H8), a2 = sub2bf(v1[g] & L, L8), a3 = sub2bf(v1[g] & H, H8);
+      const uint32_t c0 = sub2bf(y0 & L, L8), c1 = sub2bf(y0 & H, H8), c2 = sub2bf(y1 & L, L8), c3 = sub2bf(y1 & H, H8);
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         const uint32_t p0 = mul2bf(p[n][0], s0[g]), p1 = mul2bf(p[n][1], s1[g]);
-        mma16816(o[n][2 * g], v0[g] & L, v0[g] & H, v1[g] & L, v1[g] & H, p0, p1);
-        mma16816(o[n][2 * g + 1], y0 & L, y0 & H, y1 & L, y1 & H, p0, p1);
-        mma16816(o[n][2 * g], OFF, OFF16, OFF, OFF16, p0, p1);
-        mma16816(o[n][2 * g + 1], OFF, OFF16, OFF, OFF16, p0, p1);
+        mma16816(o[n][2 * g], a0, a1, a2, a3, p0, p1);
+        mma16816(o[n][2 * g + 1], c0, c1, c2, c3, p0, p1);
       }
     }
   }

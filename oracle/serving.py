@@ -16,11 +16,10 @@ def visible(n_q, n_k, window, sinks):
     return see & ((p - j < window) | (j < sinks)) if window else see
 
 
-def attention(q, k, v, window, sinks, scale=0.0, extra=None, extra_v=None):
-    """One head: q [n_q, d], k, v [n_k, d].  Returns out, lse, and sums for error
-    bounds: sum_j w_j |v_j|, the largest scale sum_c |q_c| (|k_c| + extra_c) of a
-    visible key, and sum_j w_j (|v_j| + extra_v_j).  Keys that no row sees are left
-    out."""
+def attention(q, k, v, window, sinks, scale=0.0, extra=None):
+    """One head: q [n_q, d], k, v [n_k, d].  Returns out, lse, and two sums for
+    error bounds: sum_j w_j |v_j| and the largest scale sum_c |q_c| (|k_c| + extra_c)
+    of a visible key.  Keys that no row sees are left out."""
     q, k, v = (np.asarray(x, np.float64) for x in (q, k, v))
     n_q, d = q.shape
     scale = scale or 1 / math.sqrt(d)
@@ -28,8 +27,7 @@ def attention(q, k, v, window, sinks, scale=0.0, extra=None, extra_v=None):
     used = see.any(0)
     k, v, see = k[used], v[used], see[:, used]
     big = np.abs(k) + (0 if extra is None else extra[used])
-    big_v = np.abs(v) + (0 if extra_v is None else extra_v[used])
-    out, absv, sums = (np.zeros((n_q, d)) for _ in range(3))
+    out, absv = np.zeros((n_q, d)), np.zeros((n_q, d))
     lse, size = np.full(n_q, -np.inf), np.zeros(n_q)
     if used.any():
         s = np.where(see, q @ k.T * scale, -np.inf)
@@ -39,10 +37,10 @@ def attention(q, k, v, window, sinks, scale=0.0, extra=None, extra_v=None):
         e = np.exp(s - np.where(some, m, 0)[:, None])
         total = e.sum(1)
         w = e / np.where(some, total, 1)[:, None]
-        out, absv, sums = w @ v, w @ np.abs(v), w @ big_v
+        out, absv = w @ v, w @ np.abs(v)
         with np.errstate(divide="ignore"):
             lse = np.where(some, m + np.log(total), -np.inf)
-    return out, lse, absv, size, sums
+    return out, lse, absv, size
 
 
 # ---------------------------------------------------------------------------

@@ -12,10 +12,9 @@ output's rounding u |o|, and sums of n terms n 2^-24.  The cache's K enters as
 sum of a 32-channel group is then at most sum |q_c| (|code_c| + 8) times its scale,
 so e counts |k_c| + 8 s_c in the place of |k_c|, with 3 x 32 products, 32 terms of the
 sum of q, the offset, the scale and the 4 groups: below (d + 8) roundings of 2^-24 for
-d = 128 and below 140 for either d.  Its V enters as (code + 8) too, with 8 sum w taken off
-by the next product, so that O's partial sums reach sum w s (|code| + 8): each of the two
-products of 16 tokens, and each joining of parts, rounds (or cuts) that by 2^-23 at most,
-n / 8 + 16 of them.
+d = 128 and below 140 for either d.
+O's partial sums round (or are cut) by 2^-23 of sum w |v| at most with each product of 16
+tokens and each joining of parts, n / 16 + 16 of them.
 """
 
 import math
@@ -50,12 +49,12 @@ def i32(torch, x):
 
 def check_rows(out, lse, want, d, n, dtype, roundings):
     """One head's rows against attention()'s result; roundings: bf16 roundings of a weight."""
-    o, l, absv, size, sums = want
+    o, l, absv, size = want
     assert np.isfinite(out).all()
     e = (d + 8) * 2.0 ** -24 * size[:, None]
     rel = 2 * e + 2.0 ** -21 + n * 2.0 ** -23 + roundings * 2.0 ** -8 * (1 + 2.0 ** -7)
     last = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -23
-    off = rel * absv + (n / 8 + 16) * 2.0 ** -23 * sums
+    off = (rel + (n / 16 + 16) * 2.0 ** -23) * absv
     assert (np.abs(out - o) <= last * (np.abs(o) + off) + off + 1e-38).all(), np.abs(out - o).max()
     none = np.isinf(l)
     assert np.array_equal(np.isneginf(lse), none) and (out[none] == 0).all()
@@ -304,7 +303,7 @@ def paged(torch, sa, c, seed=0):
         k, v = (torch.randn(n, Hkv, d, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
         slots = torch.tensor([order[used + i // page] * page + i % page for i in range(n)], dtype=torch.int32, device="cuda")
         sa.kv4_append(k, v, slots, cache)
-        vals.append([S.values(*S.quantise(f64(x))) for x in (k, v)] + [8 * np.repeat(S.quantise(f64(x))[1], 32, -1) for x in (k, v)])
+        vals.append([S.values(*S.quantise(f64(x))) for x in (k, v)] + [8 * np.repeat(S.quantise(f64(k))[1], 32, -1)])
         used += blocks[b]
     q = (torch.randn(sum(nq) + 2, Hq, d, device="cuda", generator=g) * 1.5).to(torch.bfloat16)
     cu = i32(torch, [sum(nq[:i]) for i in range(len(nq) + 1)])
@@ -329,8 +328,8 @@ def test_kv4_attn(torch, sa, c):
     o, l, qn, at = f64(out), f64(lse), f64(q), 0
     for b, (n, k) in enumerate(zip(nq, nk)):
         for h in range(Hq):
-            kh, vh, ek, ev = (x[:, h * Hkv // Hq] for x in vals[b])
-            want = S.attention(qn[at:at + n, h], kh, vh, window, sinks, extra=ek, extra_v=ev)
+            kh, vh, extra = (x[:, h * Hkv // Hq] for x in vals[b])
+            want = S.attention(qn[at:at + n, h], kh, vh, window, sinks, extra=extra)
             check_rows(o[at:at + n, h], l[at:at + n, h], want, 132, k, "bf16", 2)
         at += n
     assert (o[at:] == 7).all() and (l[at:] == 7).all()
@@ -538,7 +537,7 @@ def test_steps_together(torch, sa):
     cache.pages.fill_(255)
     rope = sa.Rope(64, layout="half")
     ws = sa.workspace(sa.kv4_attn_workspace(cache, Hq), "cuda")
-    past = [[np.zeros((0, Hkv, d))] * 4 for _ in range(B)]
+    past = [[np.zeros((0, Hkv, d))] * 3 for _ in range(B)]
     q_in, k_in = (torch.zeros(140, h, d, dtype=torch.bfloat16, device="cuda") for h in (Hq, Hkv))
     v_in, out = torch.zeros_like(k_in), torch.zeros_like(q_in)
     lse = torch.zeros(140, Hq, device="cuda")
@@ -559,10 +558,10 @@ def test_steps_together(torch, sa):
             rows = slice(at, at + n)
             for i, x in enumerate((kr, v_in)):
                 past[b][i] = np.concatenate([past[b][i], S.values(*S.quantise(f64(x[rows])))])
-                past[b][2 + i] = np.concatenate([past[b][2 + i], 8 * np.repeat(S.quantise(f64(x[rows]))[1], 32, -1)])
+            past[b][2] = np.concatenate([past[b][2], 8 * np.repeat(S.quantise(f64(kr[rows]))[1], 32, -1)])
             for h in range(Hq):
-                kh, vh, ek, ev = (x[:, h * Hkv // Hq] for x in past[b])
-                want = S.attention(qn[rows, h], kh, vh, window, sinks, extra=ek, extra_v=ev)
+                kh, vh, extra = (x[:, h * Hkv // Hq] for x in past[b])
+                want = S.attention(qn[rows, h], kh, vh, window, sinks, extra=extra)
                 check_rows(o[rows, h], l[rows, h], want, 132, len(past[b][0]), "bf16", 2)
             at += n
         k.turn()
@@ -666,9 +665,9 @@ def test_offsets_past_32_bits(torch, sa):
     q = torch.randn(1, 8, 128, device="cuda", generator=g).to(torch.bfloat16)
     out, lse = torch.empty_like(q), torch.empty(1, 8, device="cuda")
     sa.kv4_attn(q, cache, i32(torch, [[29999, 29123]]), i32(torch, [200]), out, lse, cu_q=i32(torch, [0, 1]))
-    ek, ev = (8 * np.repeat(S.quantise(f64(t))[1], 32, -1) for t in x)
+    extra = 8 * np.repeat(S.quantise(f64(x[0]))[1], 32, -1)
     for h in range(8):
-        want = S.attention(f64(q[:, h]), vals[0][:, h], vals[1][:, h], 0, 0, extra=ek[:, h], extra_v=ev[:, h])
+        want = S.attention(f64(q[:, h]), vals[0][:, h], vals[1][:, h], 0, 0, extra=extra[:, h])
         check_rows(f64(out[:, h]), f64(lse[:, h]), want, 132, 200, "bf16", 2)
 
 
@@ -750,7 +749,7 @@ def test_kv4_attn_queries_of_any_size(torch, sa, size, scale):
     o, l, qn, at = f64(out), f64(lse), f64(q), 0
     for b, (n, k) in enumerate(zip(c[5], c[4])):
         for h in range(8):
-            kh, vh, ek, ev = (x[:, h // 4] for x in vals[b])
-            want = S.attention(qn[at:at + n, h], kh, vh, 30, 2, scale, extra=ek, extra_v=ev)
+            kh, vh, extra = (x[:, h // 4] for x in vals[b])
+            want = S.attention(qn[at:at + n, h], kh, vh, 30, 2, scale, extra=extra)
             check_rows(o[at:at + n, h], l[at:at + n, h], want, 132, k, "bf16", 2)
         at += n
