@@ -39,7 +39,8 @@ namespace {
 
 constexpr int kTile = 128;                 // keys of a tile, rows of a query tile
 constexpr int kThreads = 384;              // 4 helper warps, 2 x 4 softmax warps
-constexpr int kStages = 5;                 // K and V tiles in flight
+constexpr int kStages = 4;                 // K and V tiles in flight (five are no faster)
+constexpr int kOutBytes = 4096;            // a softmax warp's stage of output rows
 constexpr float kRescale = 8.0f;           // log2 units
 constexpr unsigned long long kWaitNs = 2000000000ull;
 
@@ -49,8 +50,9 @@ struct Cfg {
   static constexpr int TILE_BYTES = kTile * D * 2;
   static constexpr int CHUNK_BYTES = kTile * 128;
   static constexpr int OFF_KV = 2 * TILE_BYTES;
-  static constexpr int OFF_CTL = OFF_KV + kStages * TILE_BYTES;
-  static constexpr int SMEM = OFF_CTL + 3072;
+  static constexpr int OFF_OUT = OFF_KV + kStages * TILE_BYTES;   // 8 warps' output stages
+  static constexpr int OFF_CTL = OFF_OUT + 8 * kOutBytes;
+  static constexpr int SMEM = OFF_CTL + 1024;
 };
 static_assert(Cfg<128>::SMEM <= 227 * 1024, "shared memory above the 227 KB a CTA may use");
 
@@ -83,7 +85,7 @@ struct Ctl {
   volatile uint32_t abort;
   Unit ring[4];
 };
-static_assert(sizeof(Ctl) <= 3072, "control block too large");
+static_assert(sizeof(Ctl) <= 1024, "control block too large");
 
 struct Params {
   uint16_t* out;
@@ -331,6 +333,7 @@ __device__ void softmax_rows(const Params& p, Ctl* c, uint8_t* smem, uint32_t tm
   using C = Cfg<D>;
   const int row = wq * 32 + lane;
   const uint32_t to = tm + 256 * w + ((uint32_t)(wq * 32) << 16), ts = to + 128;
+  const uint32_t stage = smem_u32(smem) + C::OFF_OUT + (4 * w + wq) * kOutBytes;
   const float sc = p.scale_log2;
   uint32_t it0 = 0, ns = 0, no = 0;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -437,9 +440,9 @@ __device__ void softmax_rows(const Params& p, Ctl* c, uint8_t* smem, uint32_t tm
       l = l * corr + (a + b);
     }
     it0 += 2 * n;
-    const int r = rows.row0 + row, live = rows.live;
-    const bool valid = r < u.n_q;
-    const int64_t at = (int64_t)rows.bh * p.Nq + r;
+    const int base = rows.row0 + wq * 32, r = base + lane, live = rows.live, bh = rows.bh, n_q = u.n_q;
+    const bool valid = r < n_q;
+    const int64_t at = (int64_t)bh * p.Nq + r;
     arrive(&c->u_empty[slot]);
     if (!live) continue;
     if (n > 0) {
@@ -447,31 +450,51 @@ __device__ void softmax_rows(const Params& p, Ctl* c, uint8_t* smem, uint32_t tm
       ++no;
       tc_fence_after();
     }
+    // O / l through shared memory: a lane holds a row of TMEM, and 16-byte stores
+    // of 32 rows would touch 32 lines each (5 us a unit where its tiles take 20 to
+    // 60); from the stage a store writes 4 rows of 128 bytes.
     const float inv = 1.f / l;
-    uint16_t* orow = p.out + at * D;
+    const uint32_t mine = stage + lane * 128;
 #pragma unroll 1
-    for (int x = 0; x < D / 32; ++x) {
-      float o[32];
-      if (n > 0) {
-        tmem_ld32(to + x * 32, o);
-        tmem_wait_ld();
-      }
-      if (!valid) continue;
+    for (int x = 0; x < D / 64; ++x) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint4 v = make_uint4(0, 0, 0, 0);   // a row that sees no key
-        if (l != 0.f) {
-          v.x = pack_bf16(o[8 * e + 0] * inv, o[8 * e + 1] * inv);
-          v.y = pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv);
-          v.z = pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv);
-          v.w = pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv);
+      for (int y = 0; y < 2; ++y) {
+        float o[32];
+        if (n > 0) {
+          tmem_ld32(to + x * 64 + y * 32, o);
+          tmem_wait_ld();
         }
-        *reinterpret_cast<uint4*>(orow + x * 32 + e * 8) = v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint4 v = make_uint4(0, 0, 0, 0);   // a row that sees no key
+          if (l != 0.f) {
+            v.x = pack_bf16(o[8 * e + 0] * inv, o[8 * e + 1] * inv);
+            v.y = pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv);
+            v.z = pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv);
+            v.w = pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv);
+          }
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + (((4 * y + e) ^ (lane & 7)) << 4)), "r"(v.x),
+                       "r"(v.y), "r"(v.z), "r"(v.w)
+                       : "memory");
+        }
       }
-    }
-    if (n > 0) {
-      tc_fence_before();
-      arrive(&c->o_free[w]);
+      if (n > 0 && x == D / 64 - 1) {
+        tc_fence_before();
+        arrive(&c->o_free[w]);
+      }
+      __syncwarp();
+      const int row4 = lane >> 3, chunk = lane & 7;
+      uint16_t* dst = p.out + ((int64_t)bh * p.Nq + base + row4) * D + x * 64 + chunk * 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint4 v;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(stage + (4 * i + row4) * 128 + ((chunk ^ ((4 * i + row4) & 7)) << 4))
+                     : "memory");
+        if (base + 4 * i + row4 < n_q) *reinterpret_cast<uint4*>(dst + (int64_t)4 * i * D) = v;
+      }
+      __syncwarp();
     }
     if (valid && p.lse) p.lse[at] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
   }
@@ -483,8 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  // Shared memory is full to the last 232 bytes: the base itself has to lie on
-  // the swizzle's 1024-byte boundary, as it does without static shared memory.
+  // The base has to lie on the swizzle's 1024-byte boundary, as it does without
+  // static shared memory (there is no room for a slack).
   uint8_t* smem = smem_raw;
   const uint32_t sb = smem_u32(smem);
   if (sb % 1024 != 0) {
