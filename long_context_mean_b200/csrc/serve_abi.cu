@@ -37,15 +37,19 @@ bool on_tensor_cores(const sa_window_shape& s) { return s.dtype == SA_BF16 && (s
 
 // Which of the two tensor-core kernels takes a shape.  The decode kernel splits
 // every row tile's keys over the GPU: its time goes with the 16-row tiles of all
-// kv heads times the keys, 5.7e-5 us each.  The prefill kernel's goes with the waves
-// of its 256-row units times the 128-key tiles, 1.9 us each.  So it wins above 260
-// row tiles a wave, whatever the keys: 32 query and 8 kv heads over 4096 keys, 128 new
-// tokens 68.7 (decode) and 70.4 us (prefill), 256 tokens 127 and 71; 24 heads of
-// their own, 4 sequences, 32 tokens 55 and 58, 64 tokens 100 and 58.
-bool prefill_wins(const sa_window_shape& s) {
+// kv heads times the keys, 5.7e-5 us each (d = 64: 3.6e-5), and 4 us more of launch
+// and join.  The prefill kernel's goes with the waves of its 256-row units times
+// the 128-key tiles, 1.9 us each (1.6).  So it wins above 260 (350) - 70,000 / keys
+// row tiles a wave.  32 query and 8 kv heads of 128, decode and prefill us: over
+// 4096 keys 128 tokens 69 and 70, 256 tokens 128 and 71; over 512 keys 32 tokens 12.6
+// and 14.5, 64 tokens 14.8 and 14.6, 128 tokens 19.6 and 14.7.  Heads of 64, 4096
+// keys: 128 tokens 46 and 58, 192 tokens 66 and 60.  24 heads of 128 of their own, 4
+// sequences of 4096 keys: 32 tokens 56 and 58, 64 tokens 100 and 58.
+bool prefill_wins(const sa_window_shape& s, int64_t window, int64_t sinks) {
   const int64_t group = s.Hq / s.Hkv, tiles = ceil_div(s.Nq, 128);
   const int64_t units = s.B * (group % 2 == 0 ? s.Hq / 2 * tiles : s.Hq * ceil_div(tiles, 2));
-  return s.B * s.Hkv * ceil_div(s.Nq * group, 16) > 260 * ceil_div(units, 148);
+  const int64_t keys = window > 0 ? min64(s.Nk, window + sinks + s.Nq) : s.Nk;
+  return s.B * s.Hkv * ceil_div(s.Nq * group, 16) + 70000 / keys > (s.d == 64 ? 350 : 260) * ceil_div(units, 148);
 }
 
 sa_status check_kv4(const sa_kv4_desc* d) {
@@ -123,7 +127,7 @@ sa_status sa_window_attn(const void* q, const void* k, const void* v, const sa_w
                scale > 0.f ? scale : 1.0f / std::sqrt((float)s.d), ws};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!on_tensor_cores(s) || flags == SA_FLAG_FORCE_SIMT) return launch_window_simt(a, st);
-  return flags == SA_FLAG_FORCE_PREFILL || (flags == 0 && prefill_wins(s)) ? launch_window_tc(a, st) : launch_window_decode(a, st);
+  return flags == SA_FLAG_FORCE_PREFILL || (flags == 0 && prefill_wins(s, window, sinks)) ? launch_window_tc(a, st) : launch_window_decode(a, st);
 }
 
 size_t sa_kv4_bytes(const sa_kv4_desc* desc) { return check_kv4(desc) == SA_OK ? kv4_size(*desc) : 0; }
