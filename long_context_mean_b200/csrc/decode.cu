@@ -11,10 +11,11 @@
 //  * the work of the whole batch (every sequence, kv head and row tile times its
 //    16 * SUBS-token tiles) is one line of tiles, cut into equal pieces, one per
 //    CTA, whatever the lengths: a ragged batch and one long sequence fill the
-//    GPU alike; a unit counts as some tiles more than it has (COST).  Lengths are read on the device; a piece may hold several
-//    units (sequence, row tile, kv head) and a unit several pieces.  Units that
-//    lie in one piece are finished there; parts of others go to the workspace
-//    and join_kernel adds them up in a fixed order (no atomics).
+//    GPU alike; a unit counts as some tiles more than it has (COST).  Lengths are
+//    read on the device; a piece may hold several units (sequence, row tile, kv
+//    head) and a unit several pieces.  Units that lie in one piece are finished
+//    there; parts of others go to the workspace and join_kernel adds them up in
+//    a fixed order (no atomics).
 //  * each warp streams its own tiles through its own ring of stages (bulk
 //    copies for the cache's subtiles, cp.async for rows; no block barrier in
 //    the loop) and multiplies with mma.sync m16n8k16: the
@@ -28,7 +29,8 @@
 //    32-channel partial scores in fp32, V's scales multiply P.  16 sequences of 8,000
 //    to 30,000 tokens, 312 MB: 68 us (4.6 TB/s); nibbles widened to bf16 integers by
 //    shift, AND-OR and subtraction took 108, 8-bit operands (converted back to
-//    fp16 by the compiler) 165.
+//    fp16 by the compiler) 165.  Contiguous bf16, 48 single tokens over up to 4352
+//    keys of 8 heads, 513 MB: 84 us (6.1 TB/s).
 // Rounding: P (and P times the V scale) is rounded to bf16 for the second
 // product; sums, maxima and outputs are fp32.
 #include <cuda_fp16.h>
@@ -217,13 +219,14 @@ __device__ __forceinline__ int tile_at(const Unit& u, int i) { return i < u.sink
 template <int D>
 struct Kv4 {
   static constexpr int G = D / 32, SUBS = 4, TOK = 16 * SUBS, SUB_BYTES = 576 * G, STAGE = SUBS * SUB_BYTES;
-  // 64 tokens a tile, two stages a warp, 12 warps an SM; with 32 tokens and three
-  // stages a tenth slower, with 16 warps more (their 128 registers spill).
+  // 64 tokens a tile, two stages a warp, 12 warps an SM: 68 us on the case above;
+  // 48 tokens 70, 32 tokens with three or four stages 78, with 16 warps 76.
   static constexpr int STAGES = 2, TILES = D / 16;
   static constexpr int CTAS = 3;
   // What a unit costs beside its tiles, in tiles (its lengths, queries and output
   // are a chain of memory latencies): without it a piece of many one-token
-  // sequences takes longest, 192 us where 8 takes 104 (16 sequences of 4 to 131,072).
+  // sequences takes longest, and the batch nearly twice the time: 16 sequences of 4
+  // to 131,072 tokens take 98 us with 8.
   static constexpr int COST = 8;
   // Channel of accumulator tile j's row lane / 4 (+ 8 where half).
   static __device__ __forceinline__ int channel(int j, int half, int r) { return 32 * (j >> 1) + 4 * r + 2 * (j & 1) + half; }
