@@ -331,6 +331,9 @@ __device__ void mma_issuer(const Params& p, Ctl* c, uint32_t sb, uint32_t tm) {
   __syncwarp();
 }
 
+// Bits x < n.
+__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? ~0u : (1u << max(n, 0)) - 1; }
+
 // Query tile w: thread (quarter wq, lane) owns row 32 wq + lane.
 template <int D>
 __device__ void softmax_rows(const Params& p, Ctl* c, uint8_t* smem, uint32_t tm, int w, int wq, int lane) {
@@ -386,8 +389,12 @@ __device__ void softmax_rows(const Params& p, Ctl* c, uint8_t* smem, uint32_t tm
         // (a valid row's position is below n_k)
         const int c_hi = rows.first + row - k0, c_lo = p.window ? c_hi - p.window + 1 : 0, c_s = p.sinks - k0;
 #pragma unroll
-        for (int x = 0; x < kTile; ++x)
-          if (x > c_hi || (x < c_lo && x >= c_s)) s[x] = -INFINITY;
+        for (int x = 0; x < kTile; x += 32) {
+          const uint32_t see = below(c_hi + 1 - x) & (~below(c_lo - x) | below(c_s - x));
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (!(see >> e & 1)) s[x + e] = -INFINITY;
+        }
       }
       float mx[4];
 #pragma unroll
