@@ -369,12 +369,13 @@ __device__ void softmax_rows(const Params& p, Ctl* c, uint8_t* smem, uint32_t tm
         if (!wait(&c->kv_full[itv % kStages], (itv / kStages) & 1)) return;
         const int key = k0 + row;
         if (key >= u.hi || (key < u.lo && key >= u.n_sink)) {
-          // the swizzle moves 16-byte pieces within a row's 128 bytes: the whole row is zeroed
+          // the swizzle moves 16-byte pieces within a row's 128 bytes: the whole row is
+          // zeroed, neighbouring lanes in other banks
           uint4* v = reinterpret_cast<uint4*>(smem + C::OFF_KV + (itv % kStages) * C::TILE_BYTES + row * 128);
 #pragma unroll
           for (int x = 0; x < C::CHUNKS; ++x)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[x * (C::CHUNK_BYTES / 16) + e] = make_uint4(0, 0, 0, 0);
+            for (int e = 0; e < 8; ++e) v[x * (C::CHUNK_BYTES / 16) + (e ^ (row & 7))] = make_uint4(0, 0, 0, 0);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
