@@ -24,9 +24,9 @@
 //    query tile are issued in order P V(t), S(t + 1), so S may overwrite P without
 //    a barrier, and S(t + 1)'s arrival tells that P V(t) is done.
 //  * O is rescaled only when a row's maximum grows by more than 2^8.
-// 16,384 rows, 32/8 heads of 128, window 4096, 128 sinks: 870 us, 1135 TFLOP/s of
-// visible pairs, some 3150 clocks for two tiles of 2048 clocks of mma; three padded
-// prompts of up to 2777 rows, window 1024: 115 us, where a unit of ten tiles pays
+// 16,384 rows, 32/8 heads of 128, window 4096, 128 sinks: 855 us, 1155 TFLOP/s of
+// visible pairs, some 3100 clocks for two tiles of 2048 clocks of mma; three padded
+// prompts of up to 2777 rows, window 1024: 102 us, where a unit of ten tiles pays
 // its start and its output.
 // Roundings: P is rounded to bf16 for the second product (l sums the unrounded
 // values); everything else is fp32.
@@ -370,7 +370,7 @@ __device__ void softmax_rows(const Params& p, Ctl* c, uint8_t* smem, uint32_t tm
         const int key = k0 + row;
         if (key >= u.hi || (key < u.lo && key >= u.n_sink)) {
           // the swizzle moves 16-byte pieces within a row's 128 bytes: the whole row is
-          // zeroed, neighbouring lanes in other banks
+          // zeroed, neighbouring lanes in other banks (in one, 108 us where this takes 102)
           uint4* v = reinterpret_cast<uint4*>(smem + C::OFF_KV + (itv % kStages) * C::TILE_BYTES + row * 128);
 #pragma unroll
           for (int x = 0; x < C::CHUNKS; ++x)
@@ -388,6 +388,8 @@ __device__ void softmax_rows(const Params& p, Ctl* c, uint8_t* smem, uint32_t tm
       tmem_wait_ld();
       if (!whole) {
         // (a valid row's position is below n_k)
+        // One bit a key (comparisons for every key took 2% of the 16,384 rows' time,
+        // 6% of the padded prompts').
         const int c_hi = rows.first + row - k0, c_lo = p.window ? c_hi - p.window + 1 : 0, c_s = p.sinks - k0;
 #pragma unroll
         for (int x = 0; x < kTile; x += 32) {

@@ -612,6 +612,42 @@ def test_a_captured_step_runs_on_new_inputs(torch, sa):
 
 
 # ---------------------------------------------------------------------------
+# Few sinks before a far window
+# ---------------------------------------------------------------------------
+
+FEW_SINKS = [
+    (1, 4, 2, 300, 600, 128, "bf16", 100, 1, None, None),
+    (2, 4, 2, 260, 700, 64, "bf16", 64, 32, [260, 131], [700, 400]),
+    (1, 3, 3, 400, 500, 128, "bf16", 150, 31, None, None),
+    (1, 2, 1, 257, 520, 128, "bf16", 90, 33, None, None),
+    (1, 2, 2, 513, 900, 64, "bf16", 200, 4, None, None),
+    (1, 2, 1, 128, 355, 128, "bf16", 100, 7, None, None),     # the window starts on the second tile's border
+    (1, 2, 1, 128, 354, 128, "bf16", 100, 7, None, None),     # and one key before it
+    (2, 2, 2, 300, 300, 128, "bf16", 20, 16, [300, 5], [300, 290]),
+]
+
+
+@pytest.mark.parametrize("c", FEW_SINKS, ids=lambda c: "-".join(map(str, c[:9])))
+@pytest.mark.parametrize("poison", [False, True])
+def test_window_attn_few_sinks(torch, sa, c, poison):
+    test_window_attn(torch, sa, c, 16, poison)
+
+
+def test_window_attn_few_sinks_of_any_score(torch, sa):
+    """Sinks far above and far below the window's scores, and at minus infinity."""
+    q, k, v, _, _ = window_inputs(torch, (1, 2, 1, 200, 500, 64, "bf16", 70, 3, None, None))
+    q.abs_()
+    for size in (30.0, -30.0, -math.inf):
+        k[:, :, :3] = size
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+        sa.window_attn(q, k, v, out, lse, window=70, sinks=3, flags=16)
+        o, l, qn, vn = (f64(t) for t in (out, lse, q, v))
+        kn = f64(k) if size != -math.inf else np.where(np.isinf(f64(k)), -1e30, f64(k))
+        for h in range(2):
+            check_rows(o[0, h], l[0, h], S.attention(qn[0, h], kn[0, 0], vn[0, 0], 70, 3), 64, 500, "bf16", 1)
+
+
+# ---------------------------------------------------------------------------
 # Many units, and offsets past 32 bits
 # ---------------------------------------------------------------------------
 
