@@ -94,7 +94,7 @@ __device__ __forceinline__ uint32_t code8(const uint4& x, uint16_t scale) {
   }
   // 1.5 2^11: multiples of 2^-12; 1.5 2^23 + 8: integers, with code + 8 in the low
   // bits.  The words w = 16 w + bits gather the codes and 8 times kOne's bits.
-  constexpr float kGrid = 3072.f, kOne = 12582920.f;
+  constexpr float kGrid = 0x1.8p11f, kOne = 0x1.8p23f + 8.f;
   constexpr uint32_t kBits = 0x4B400000u * 0x11111111u;
   uint32_t w = 0;
 #pragma unroll
