@@ -470,14 +470,15 @@ def _raw(stream):
 
 
 def _call_workspace(nbytes, t, name, stream):
-    """A workspace for one call on tensors like t."""
+    """A workspace for one call on tensors like t.  It comes from the pool of
+    the stream that the call runs on: a block of another stream's pool may
+    still be in use by work queued there."""
     _need(t.is_cuda, f"{name} must be on a CUDA device")
-    ws = workspace(nbytes, t.device)
-    if stream is not None:
-        import torch
-        if not torch.cuda.is_current_stream_capturing():
-            ws.record_stream(stream)     # it stays allocated until that stream has used it
-    return ws
+    if stream is None:
+        return workspace(nbytes, t.device)
+    import torch
+    with torch.cuda.stream(stream):
+        return workspace(nbytes, t.device)
 
 
 def make_window_shape(q, k) -> WindowShape:

@@ -789,3 +789,45 @@ def test_kv4_attn_queries_of_any_size(torch, sa, size, scale):
             want = S.attention(qn[at:at + n, h], kh, vh, 30, 2, scale, extra=extra)
             check_rows(o[at:at + n, h], l[at:at + n, h], want, 132, k, "bf16", 2)
         at += n
+
+
+# ---------------------------------------------------------------------------
+# Workspaces that a call allocates, beside work queued on another stream
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("op", ["decode", "prefill", "kv4"])
+def test_a_calls_own_workspace_is_not_shared_with_queued_work(torch, sa, op):
+    """The current stream holds a long queue that still fills and reads a freed temporary of the workspace's
+    size, while the call runs on a side stream without `ws`: both keep their results."""
+    if op == "kv4":
+        c = (32, 8, 128, 64, [3000], [1], 0, 0)
+        q, cache, table, kv_len, cu, _ = paged(torch, sa, c)
+        q, table = q[:1], table.cuda()
+        n = sa.kv4_attn_workspace(cache, 32)
+
+        def call(out, **kw):
+            sa.kv4_attn(q, cache, table, kv_len, out, cu_q=cu, **kw)
+    else:
+        Nq, Nk, flags = (1, 3000, 8) if op == "decode" else (700, 900, 16)
+        q, k, v, _, _ = window_inputs(torch, (2, 32, 8, Nq, Nk, 128, "bf16", 300, 5, None, None))
+        n = sa.window_attn_workspace(q, k, v)
+
+        def call(out, **kw):
+            sa.window_attn(q, k, v, out, window=300, sinks=5, flags=flags, **kw)
+    want, out = torch.empty_like(q), torch.empty_like(q)
+    call(want)
+    side, kept = torch.cuda.Stream(), torch.empty(n, dtype=torch.uint8, device="cuda")
+    x = torch.randn(2048, 2048, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(20):
+        out.zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        temp = torch.empty(n, dtype=torch.uint8, device="cuda")
+        for _ in range(10):
+            x = torch.clamp(x @ x, -1, 1)
+            temp.fill_(i)
+        kept.copy_(temp)
+        del temp
+        call(out, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and (kept == i).all()

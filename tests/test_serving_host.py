@@ -224,3 +224,28 @@ def test_plain_plan_keeps_every_page_once():
         assert sorted(held + free) == list(range(num))
         live = [s for s in r["slots"] if s >= 0]
         assert len(set(live)) == len(live)
+
+
+# ---------------------------------------------------------------------------
+# Workspaces of a call
+# ---------------------------------------------------------------------------
+
+def test_a_calls_own_workspace_comes_from_the_stream_that_it_runs_on(monkeypatch):
+    """A block of the current stream's pool may still be in use by work queued there while `stream` writes it."""
+    import contextlib
+    from types import SimpleNamespace
+
+    import torch
+    current = ["current"]
+
+    @contextlib.contextmanager
+    def use(stream):
+        current.append(stream)
+        yield
+        current.pop()
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    monkeypatch.setattr(sa, "workspace", lambda n, device: SimpleNamespace(n=n, pool=current[-1]))
+    t = SimpleNamespace(is_cuda=True, device="cuda:0")
+    ws = sa._call_workspace(512, t, "q", "side")
+    assert (ws.n, ws.pool, current) == (512, "side", ["current"])
+    assert sa._call_workspace(512, t, "q", None).pool == "current"
