@@ -543,7 +543,9 @@ sa_status sa_kv4_read(const void* cache, const sa_kv4_desc* desc, const int32_t*
  * window and sinks as above.  Few new tokens a sequence are what it is made
  * for: every 16 rows (tokens times query heads of a kv head) read the cache
  * once.  Queries above 2^100 in magnitude, and values of V above 2^50, overflow;
- * weights times scales of V below 2^-57 are lost.  T * Hq below 2^31.  ws:
+ * weights times scales of V below 2^-57 are lost.  T * Hq below 2^31.  Should
+ * a wait for a copy run out (2 s; status SA_ERR_TIMEOUT), its block stops:
+ * the rows that it works on stay as they were or become NaN.  ws:
  * sa_kv4_attn_workspace() bytes, 256-byte aligned, not to be shared by calls
  * that overlap on the GPU. */
 size_t sa_kv4_attn_workspace(const sa_kv4_desc* desc, int64_t Hq);

@@ -50,6 +50,7 @@ constexpr int kJoinThreads = 256;
 // The reference maximum moves (and O with it) only when a score passes it by
 // 2^8: with every new maximum a fifth of the tiles would rescale 64 numbers.
 constexpr float kRescale = 8.f;
+constexpr unsigned long long kWaitNs = 2000000000ull, kTestWaitNs = 10000000ull;
 
 // What a worker leaves for join_kernel.
 struct Piece {
@@ -79,6 +80,8 @@ struct DecodeArgs {
   int32_t num_pages, page_bytes, window, sinks;
   int32_t B, Hkv, group, lg_page;
   float scale_log2;
+  int32_t stall;                 // test hook: this block's copies are never reported whole; -1: none
+  unsigned long long wait_ns;    // limit of every wait
 };
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -114,17 +117,26 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
                : "memory");
   return ok != 0;
 }
-// Bounded wait for a copy in flight (2 s; a copy always arrives, so the bound
-// only keeps a broken device from holding the kernel).
-__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, int32_t* status) {
-  if (bar_try(bar, parity)) return;
-  unsigned long long t0, t1;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-  while (!bar_try(bar, parity)) {
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t1));
-    if (t1 - t0 > 2000000000ull) {
+__device__ __forceinline__ unsigned long long clock_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// Bounded wait for a copy in flight (a copy always arrives, so the bound only
+// keeps a broken device from holding the kernel).  False where the time ran out,
+// here (then the block's abort flag is set and the status raised) or in
+// another warp's wait.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int32_t* abort, unsigned long long limit,
+                                         int32_t* status) {
+  if (bar_try(bar, parity)) return true;
+  const unsigned long long t0 = clock_ns();
+  for (;;) {
+    if (bar_try(bar, parity)) return true;
+    if (*abort) return false;
+    if (clock_ns() - t0 > limit) {
+      *abort = 1;
       raise_status(status, SA_ERR_TIMEOUT);
-      return;
+      return false;
     }
   }
 }
@@ -526,12 +538,14 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
   __shared__ int found_b;
   __shared__ float wm[kWarps][ROWS], wl[kWarps][ROWS];
   __shared__ __align__(8) uint64_t bars[kWarps][F::STAGES];
+  __shared__ volatile int32_t abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, t4 = lane & 3;
   if (F::kBulk && tid < kWarps * F::STAGES) {
-    bar_init(smem_addr(&bars[0][0] + tid), F::SUBS);
+    bar_init(smem_addr(&bars[0][0] + tid), F::SUBS + ((int)blockIdx.x == a.stall));
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (tid == 0) abort = 0;
 
   // Where this piece of the line of tiles starts.
   const int per_thread = (a.B + kThreads - 1) / kThreads;
@@ -649,11 +663,23 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
     }
 
     for (int i = 0; i < mine; ++i) {
-      if (F::kBulk)
-        bar_wait(bar + out * 8, phase, a.status);
-      else
+      if constexpr (F::kBulk) {
+        if (!__all_sync(0xffffffffu, bar_wait(bar + out * 8, phase, &abort, a.wait_ns, a.status))) {
+          // A wait has run out: nothing more is fetched, and what is under way lands first.
+          const unsigned long long t0 = clock_ns();
+          for (; i < sent; ++i) {
+            while (!bar_try(bar + out * 8, phase) && clock_ns() - t0 < a.wait_ns) {}
+            if (++out == F::STAGES) {
+              out = 0;
+              phase ^= 1;
+            }
+          }
+          break;
+        }
+      } else {
         cp_wait<F::STAGES - 2>();
-      __syncwarp();
+        __syncwarp();
+      }
       const uint8_t* st = ring_p + out * F::STAGE;
       send();
       if (++out == F::STAGES) {
@@ -749,6 +775,15 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
         }
       }
     __syncthreads();
+    const bool begins = i0 == 0, ends = i1 == tl;
+    const int64_t slot = (int64_t)blockIdx.x * 2 + (begins ? 1 : 0);
+    // (no wait lies between this barrier and the next, so all threads see the same)
+    if (F::kBulk && abort) {
+      // The rows of this piece's units stay as they were; those of the unit that
+      // goes through it become NaN.
+      if (!begins && tid < ROWS) *reinterpret_cast<float2*>(a.part_ml + (slot * ROWS + tid) * 2) = make_float2(-INFINITY, NAN);
+      break;
+    }
     float* os = reinterpret_cast<float*>(sm);   // [warp][ROWS][D + 4]
     constexpr int OS = D + 4;
 #pragma unroll
@@ -759,8 +794,6 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? F::CTAS : 2) decode_kernel
         for (int e = 0; e < 4; ++e)
           os[(warp * ROWS + 8 * n + 2 * t4 + (e & 1)) * OS + F::channel(j, e >> 1, r)] = o[n][j][e] * F::gain(e >> 1);
     __syncthreads();
-    const bool begins = i0 == 0, ends = i1 == tl;
-    const int64_t slot = (int64_t)blockIdx.x * 2 + (begins ? 1 : 0);
     for (int e = tid; e < ROWS * (D / 8); e += kThreads) {
       const int row = e / (D / 8), c8 = e % (D / 8);
       float mx = wm[0][row];
@@ -947,6 +980,8 @@ sa_status launch_kv4_attn(const Kv4AttnArgs& x, cudaStream_t st) {
   a.group = (int32_t)(x.Hq / x.desc.Hkv);
   while ((1LL << a.lg_page) < x.desc.page) ++a.lg_page;
   a.scale_log2 = x.scale * kLog2e;
+  a.stall = x.stall;
+  a.wait_ns = x.stall >= 0 ? kTestWaitNs : kWaitNs;
   // Two column tiles (16 rows) a unit where the average sequence has more than 8 rows.
   const int nq = x.T * a.group > 8 * x.B ? 2 : 1;
   const int64_t row_tiles = ceil_div(x.T * a.group, 8 * nq) + x.B;

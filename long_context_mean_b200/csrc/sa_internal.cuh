@@ -217,6 +217,7 @@ struct Kv4AttnArgs {
   int64_t window, sinks;
   float scale;
   void* ws;
+  int32_t stall;           // test hook (sa_kv4_attn_stalled): a block, or -1
 };
 size_t decode_ws_bytes(int64_t d);
 sa_status launch_window_decode(const WindowArgs& a, cudaStream_t st);   // bf16, d in {64, 128}

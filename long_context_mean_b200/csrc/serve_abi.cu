@@ -89,6 +89,41 @@ bool disjoint_rows(const int64_t* strides, const int64_t* sizes, int n, int64_t 
   return true;
 }
 
+sa_status kv4_attn(int32_t stall, const void* q, int64_t T, int64_t Hq, const int64_t q_strides[2], const int32_t* cu_q,
+                   int64_t B, const void* cache, const sa_kv4_desc* desc, const int32_t* table, int64_t max_blocks,
+                   const int32_t* kv_len, int64_t window, int64_t sinks, float scale, void* out, float* lse,
+                   int32_t* status, void* ws, size_t ws_bytes, void* stream) {
+  if (sa_status e = check_kv4(desc)) return e;
+  if (sa_status e = check_window(window, sinks, scale)) return e;
+  if (T < 0 || B < 0 || max_blocks < 0 || Hq <= 0) return set_error(SA_ERR_INVALID_ARG, "negative size");
+  if (Hq % desc->Hkv != 0) return set_error(SA_ERR_INVALID_ARG, "Hq must be a multiple of Hkv");
+  if (T > kInt32 / 2 || B > kInt32 / 2 || Hq > 65535 || T * Hq > kInt32 || max_blocks > kInt32 / 2 / desc->page)
+    return set_error(SA_ERR_UNSUPPORTED, "sizes too large");
+  if (T == 0 || B == 0) return SA_OK;   // no row
+  if (max_blocks == 0) return set_error(SA_ERR_INVALID_ARG, "max_blocks must be positive");
+  if (!q || !q_strides || !cu_q || !cache || !table || !kv_len || !out)
+    return set_error(SA_ERR_INVALID_ARG, "NULL argument to sa_kv4_attn");
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(cache, 16))
+    return set_error(SA_ERR_INVALID_ARG, "q, out and the cache must be 16-byte aligned");
+  if (q_strides[0] < 0 || q_strides[1] < 0 || q_strides[0] % 8 || q_strides[1] % 8)
+    return set_error(SA_ERR_INVALID_ARG, "q strides must be non-negative multiples of 8 elements");
+  const int64_t sizes[2] = {T, Hq};
+  const size_t qb = 2 * span(q_strides, sizes, 2, desc->d), ob = (size_t)T * Hq * desc->d * 2, lb = (size_t)T * Hq * 4;
+  if (ranges_overlap(out, ob, q, qb) || ranges_overlap(out, ob, cache, kv4_size(*desc)) ||
+      (lse && (ranges_overlap(lse, lb, q, qb) || ranges_overlap(lse, lb, cache, kv4_size(*desc)) ||
+               ranges_overlap(lse, lb, out, ob))))
+    return set_error(SA_ERR_INVALID_ARG, "out and lse must overlap neither q, the cache nor each other");
+  const size_t need = sa_kv4_attn_workspace(desc, Hq);
+  if (!ws || ws_bytes < need || !aligned(ws, 256))
+    return set_error(SA_ERR_WORKSPACE, "sa_kv4_attn needs %zu bytes of 256-byte aligned workspace", need);
+  if (sa_status e = check_device()) return e;
+  if (!is_sm100()) return set_error(SA_ERR_UNSUPPORTED, "sa_kv4_attn needs an sm_100 device");
+  Kv4AttnArgs a{q, cache, cu_q, table, kv_len, out, lse, status, *desc, T, Hq, B, max_blocks,
+                {q_strides[0], q_strides[1]}, window, sinks,
+                scale > 0.f ? scale : 1.0f / std::sqrt((float)desc->d), ws, stall};
+  return launch_kv4_attn(a, static_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -179,35 +214,20 @@ sa_status sa_kv4_attn(const void* q, int64_t T, int64_t Hq, const int64_t q_stri
                       int64_t B, const void* cache, const sa_kv4_desc* desc, const int32_t* table,
                       int64_t max_blocks, const int32_t* kv_len, int64_t window, int64_t sinks, float scale,
                       void* out, float* lse, int32_t* status, void* ws, size_t ws_bytes, void* stream) {
-  if (sa_status e = check_kv4(desc)) return e;
-  if (sa_status e = check_window(window, sinks, scale)) return e;
-  if (T < 0 || B < 0 || max_blocks < 0 || Hq <= 0) return set_error(SA_ERR_INVALID_ARG, "negative size");
-  if (Hq % desc->Hkv != 0) return set_error(SA_ERR_INVALID_ARG, "Hq must be a multiple of Hkv");
-  if (T > kInt32 / 2 || B > kInt32 / 2 || Hq > 65535 || T * Hq > kInt32 || max_blocks > kInt32 / 2 / desc->page)
-    return set_error(SA_ERR_UNSUPPORTED, "sizes too large");
-  if (T == 0 || B == 0) return SA_OK;   // no row
-  if (max_blocks == 0) return set_error(SA_ERR_INVALID_ARG, "max_blocks must be positive");
-  if (!q || !q_strides || !cu_q || !cache || !table || !kv_len || !out)
-    return set_error(SA_ERR_INVALID_ARG, "NULL argument to sa_kv4_attn");
-  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(cache, 16))
-    return set_error(SA_ERR_INVALID_ARG, "q, out and the cache must be 16-byte aligned");
-  if (q_strides[0] < 0 || q_strides[1] < 0 || q_strides[0] % 8 || q_strides[1] % 8)
-    return set_error(SA_ERR_INVALID_ARG, "q strides must be non-negative multiples of 8 elements");
-  const int64_t sizes[2] = {T, Hq};
-  const size_t qb = 2 * span(q_strides, sizes, 2, desc->d), ob = (size_t)T * Hq * desc->d * 2, lb = (size_t)T * Hq * 4;
-  if (ranges_overlap(out, ob, q, qb) || ranges_overlap(out, ob, cache, kv4_size(*desc)) ||
-      (lse && (ranges_overlap(lse, lb, q, qb) || ranges_overlap(lse, lb, cache, kv4_size(*desc)) ||
-               ranges_overlap(lse, lb, out, ob))))
-    return set_error(SA_ERR_INVALID_ARG, "out and lse must overlap neither q, the cache nor each other");
-  const size_t need = sa_kv4_attn_workspace(desc, Hq);
-  if (!ws || ws_bytes < need || !aligned(ws, 256))
-    return set_error(SA_ERR_WORKSPACE, "sa_kv4_attn needs %zu bytes of 256-byte aligned workspace", need);
-  if (sa_status e = check_device()) return e;
-  if (!is_sm100()) return set_error(SA_ERR_UNSUPPORTED, "sa_kv4_attn needs an sm_100 device");
-  Kv4AttnArgs a{q, cache, cu_q, table, kv_len, out, lse, status, *desc, T, Hq, B, max_blocks,
-                {q_strides[0], q_strides[1]}, window, sinks,
-                scale > 0.f ? scale : 1.0f / std::sqrt((float)desc->d), ws};
-  return launch_kv4_attn(a, static_cast<cudaStream_t>(stream));
+  return kv4_attn(-1, q, T, Hq, q_strides, cu_q, B, cache, desc, table, max_blocks, kv_len, window, sinks, scale, out,
+                  lse, status, ws, ws_bytes, stream);
+}
+
+// Not part of the interface: sa_kv4_attn with a wait that runs out, for its test.  The
+// copies of block `stall` are never reported whole, the limit is 10 ms instead of 2 s,
+// and the status word gets SA_ERR_TIMEOUT.
+sa_status sa_kv4_attn_stalled(int32_t stall, const void* q, int64_t T, int64_t Hq, const int64_t q_strides[2],
+                              const int32_t* cu_q, int64_t B, const void* cache, const sa_kv4_desc* desc,
+                              const int32_t* table, int64_t max_blocks, const int32_t* kv_len, int64_t window,
+                              int64_t sinks, float scale, void* out, float* lse, int32_t* status, void* ws,
+                              size_t ws_bytes, void* stream) {
+  return kv4_attn(stall, q, T, Hq, q_strides, cu_q, B, cache, desc, table, max_blocks, kv_len, window, sinks, scale, out,
+                  lse, status, ws, ws_bytes, stream);
 }
 
 sa_status sa_rope_frequencies(const sa_rope_scaling* desc, uint64_t* freqs, float* magnitude) {

@@ -831,3 +831,41 @@ def test_a_calls_own_workspace_is_not_shared_with_queued_work(torch, sa, op):
         call(out, stream=side)
         torch.cuda.synchronize()
         assert torch.equal(out, want) and (kept == i).all()
+
+
+# ---------------------------------------------------------------------------
+# Waits that run out
+# ---------------------------------------------------------------------------
+
+def test_kv4_attn_timeout_path_reports_and_recovers(torch, sa):
+    """A block whose copies are never reported whole: its wait runs out (after 10 ms here), it stops, and the status
+    says so.  One sequence over 20,000 keys is 8 units of 8 + 313 tiles, 6 a block: block 1 begins the first kv head's
+    unit, whose rows then stay as they were; block 2 is inside it, and its rows become NaN.  All others are untouched
+    by it, and later calls run as before."""
+    import ctypes
+    c = (32, 8, 128, 64, [20000], [1], 0, 0)
+    q, cache, table, kv_len, cu, _ = paged(torch, sa, c)
+    q, table = q[:1], table.cuda()
+    want, want_lse = torch.empty_like(q), torch.empty(1, 32, device="cuda")
+    sa.kv4_attn(q, cache, table, kv_len, want, want_lse, cu_q=cu)
+    ws = sa.workspace(sa.kv4_attn_workspace(cache, 32), "cuda")
+    lib = sa.load()
+    fn = lib.sa_kv4_attn_stalled
+    fn.restype, fn.argtypes = ctypes.c_int32, [ctypes.c_int32] + lib.sa_kv4_attn.argtypes
+    status = i32(torch, [0])
+    for block in (1, 2, 2, 1):
+        out, lse = torch.full_like(q, 7.0), torch.full((1, 32), 7.0, device="cuda")
+        status.zero_()
+        p = lambda t: ctypes.c_void_p(t.data_ptr())   # noqa: E731
+        code = fn(block, p(q), 1, 32, ctypes.byref((ctypes.c_int64 * 2)(32 * 128, 128)), p(cu), 1, p(cache.pages),
+                  ctypes.byref(cache.desc), p(table), table.shape[1], p(kv_len), 0, 0, 0.0, p(out), p(lse), p(status),
+                  p(ws), ws.numel(), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        assert code == sa.SA_OK and sa.read_status(status) == sa.SA_ERR_TIMEOUT
+        assert torch.equal(out[:, 4:], want[:, 4:]) and torch.equal(lse[:, 4:], want_lse[:, 4:])
+        if block == 1:
+            assert (out[:, :4] == 7).all() and (lse[:, :4] == 7).all()
+        else:
+            assert torch.isnan(out[:, :4]).all() and torch.isnan(lse[:, :4]).all()
+        status.zero_()
+        sa.kv4_attn(q, cache, table, kv_len, out, lse, cu_q=cu, ws=ws, status=status)
+        assert sa.read_status(status) == 0 and torch.equal(out, want) and torch.equal(lse, want_lse)
