@@ -560,7 +560,8 @@ sa_status sa_kv4_attn(const void* q, int64_t T, int64_t Hq, const int64_t q_stri
  * its channels i and i + rot_dim / 2 (SA_ROPE_HALF) or 2 i and 2 i + 1
  * (SA_ROPE_INTERLEAVED); the other channels are copied.  inverse = 1 turns
  * back by the same angle (still times magnitude): the gradient of the forward
- * rotation.  Angles are exact modulo a turn for every int32 position.
+ * rotation.  The angle is within 2^-24 rad of p * w_i for every int32
+ * position.
  * Strides are in elements, {batch, token, head}, channels contiguous; pos is
  * device int32, token n of batch b at pos[b * pos_stride + n] (0: one row of
  * positions for all).  k may be NULL (Hk = 0).  q_out may be q and k_out may

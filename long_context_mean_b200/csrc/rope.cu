@@ -6,9 +6,10 @@
 //
 // The angle of a far position needs more bits than a float has: p = 10^6 with
 // w = 1 would be off by 0.03 rad.  Frequencies are therefore held as turns per
-// position in 64-bit fixed point (f = round(w / 2 pi * 2^64)): p * f modulo
-// 2^64 is the exact fraction of a turn (error p * 2^-65), one integer multiply,
-// and its top 32 bits are split into quarter turns and a rest for sincospif.
+// position in 64-bit fixed point (f = w / 2 pi * 2^64, good to a few units): p * f
+// modulo 2^64 is the fraction of a turn (below 5e-9 rad off at 2^31), one integer
+// multiply, and its top 32 bits are split into quarter turns and a rest for
+// sincospif (2.5e-8 rad).
 //
 // Bound by HBM: x read once, y written once.  A CTA takes TOK tokens: it
 // computes their cos and sin once into shared memory (one pair per thread) and
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     const int64_t p = a.pos[b * a.pos_sb + (t - b * a.N)];
     const uint64_t phase = (uint64_t)p * a.freqs[f];
     // The nearest quarter turn and the rest in [-1/4, 1/4) half turns: the
-    // rest's rounding to 24 bits is then below 5e-8 rad.
+    // rest's rounding to 24 bits is then at most 2^-27 half turns, 2.4e-8 rad.
     const int32_t top = (int32_t)(phase >> 32);
     const uint32_t quarter = ((uint32_t)top + 0x20000000u) >> 30;
     float s, c;

@@ -1,5 +1,6 @@
 // The C ABI of the serving operators: argument validation and dispatch.  Every
 // check runs on the host before any work is enqueued.
+#include <cfloat>
 #include <cmath>
 
 #include "sa_internal.cuh"
@@ -235,7 +236,7 @@ sa_status sa_rope_frequencies(const sa_rope_scaling* desc, uint64_t* freqs, floa
   const int32_t rot_dim = desc->rot_dim, scaling = desc->scaling;
   const double factor = desc->factor, beta_fast = desc->beta_fast, beta_slow = desc->beta_slow;
   const int64_t original_len = desc->original_len;
-  double base = desc->base;
+  const double base = desc->base;
   if (rot_dim < 2 || rot_dim % 2 || rot_dim > 1024) return set_error(SA_ERR_INVALID_ARG, "rot_dim must be even, 2 .. 1024");
   if (!(base > 1.0) || std::isinf(base)) return set_error(SA_ERR_INVALID_ARG, "base must be above 1 and finite");
   if (scaling < SA_ROPE_SCALE_NONE || scaling > SA_ROPE_SCALE_YARN)
@@ -243,7 +244,6 @@ sa_status sa_rope_frequencies(const sa_rope_scaling* desc, uint64_t* freqs, floa
   if (scaling != SA_ROPE_SCALE_NONE && (!(factor >= 1.0) || std::isinf(factor)))
     return set_error(SA_ERR_INVALID_ARG, "factor must be at least 1 and finite");
   const double two_pi = 6.283185307179586476925286766559;
-  if (scaling == SA_ROPE_SCALE_NTK && rot_dim > 2) base *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
   double lo = 0, hi = 0;
   *magnitude = 1.f;
   if (scaling == SA_ROPE_SCALE_YARN) {
@@ -257,15 +257,20 @@ sa_status sa_rope_frequencies(const sa_rope_scaling* desc, uint64_t* freqs, floa
     hi = std::fmin(rot_dim - 1.0, std::ceil(pair(beta_slow)));
     *magnitude = (float)(0.1 * std::log(factor) + 1.0);
   }
+  // In 64 bits of mantissa: a frequency is then off by less than 4 units of 2^-64 turns, and
+  // the angle of a position of 2^31 by less than 3e-9 rad (53 bits would leave 3e-7).
+  static_assert(LDBL_MANT_DIG >= 64, "the frequencies need a long double of 64 bits");
+  long double b = base;
+  if (scaling == SA_ROPE_SCALE_NTK && rot_dim > 2) b *= std::pow((long double)factor, (long double)rot_dim / (rot_dim - 2));
   for (int i = 0; i < rot_dim / 2; ++i) {
-    double w = std::pow(base, -2.0 * i / rot_dim);
+    long double w = std::pow(b, -2.0L * i / rot_dim);
     if (scaling == SA_ROPE_SCALE_LINEAR) w /= factor;
     if (scaling == SA_ROPE_SCALE_YARN) {
-      const double r = std::fmin(1.0, std::fmax(0.0, (i - lo) / std::fmax(hi - lo, 1e-3)));
+      const long double r = std::fmin(1.0L, std::fmax(0.0L, (i - (long double)lo) / std::fmax((long double)hi - lo, 1e-3L)));
       w = w * (1 - r) + w / factor * r;
     }
     // w <= 1: below 2^62 in units of 2^-64 turns
-    freqs[i] = (uint64_t)std::llround(std::ldexp(w / two_pi, 64));
+    freqs[i] = (uint64_t)std::llround(std::ldexp(w / 6.283185307179586476925286766559005768L, 64));
   }
   return SA_OK;
 }

@@ -3,9 +3,13 @@ positions, the 4-bit cache's rows and pages, and the cache plan."""
 
 from __future__ import annotations
 
+import decimal
 import math
+from decimal import Decimal as D
 
 import numpy as np
+
+TWO_PI = D("6.28318530717958647692528676655900576839433879875021164194989")
 
 
 def visible(n_q, n_k, window, sinks):
@@ -62,6 +66,31 @@ def rope_frequencies(rot, base=10000.0, scaling="none", factor=1.0, original_len
     lo, hi = max(0, math.floor(pair(beta_fast))), min(rot - 1, math.ceil(pair(beta_slow)))
     r = np.clip((np.arange(rot // 2) - lo) / max(hi - lo, 1e-3), 0, 1)
     return w * (1 - r) + w / factor * r, 0.1 * math.log(factor) + 1
+
+
+def rope_turns(rot, base=10000.0, scaling="none", factor=1.0, original_len=0, beta_fast=32.0, beta_slow=1.0):
+    """The frequencies in turns per position, as decimal fractions of 60 digits."""
+    with decimal.localcontext(decimal.Context(prec=60)):
+        base, factor = D(base), D(factor)
+        if scaling == "ntk" and rot > 2:
+            base *= (factor.ln() * rot / (rot - 2)).exp()
+        w = [(base.ln() * -2 * i / rot).exp() for i in range(rot // 2)]
+        if scaling == "linear":
+            w = [x / factor for x in w]
+        if scaling == "yarn":
+            def pair(turns):
+                return rot * (D(original_len) / (D(turns) * TWO_PI)).ln() / (2 * base.ln())
+            lo, hi = max(0, math.floor(pair(beta_fast))), min(rot - 1, math.ceil(pair(beta_slow)))
+            r = [min(D(1), max(D(0), D(i - lo) / (D(hi - lo) if hi > lo else D("0.001")))) for i in range(rot // 2)]
+            w = [x * (1 - y) + x / factor * y for x, y in zip(w, r)]
+        return [x / TWO_PI for x in w]
+
+
+def far_angles(pos, turns):
+    """[T, pairs]: the angles of positions (of any size and sign) as radians within half a turn."""
+    with decimal.localcontext(decimal.Context(prec=60)):
+        rest = [[(int(p) * t) % 1 for t in turns] for p in pos]
+        return np.array([[float((r - round(r)) * TWO_PI) for r in row] for row in rest])
 
 
 def rope(x, pos, w, mag, layout, inverse=False):

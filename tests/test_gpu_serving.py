@@ -869,3 +869,28 @@ def test_kv4_attn_timeout_path_reports_and_recovers(torch, sa):
         status.zero_()
         sa.kv4_attn(q, cache, table, kv_len, out, lse, cu_q=cu, ws=ws, status=status)
         assert sa.read_status(status) == 0 and torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions at the ends of their range
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("rot,kw", [(64, {}), (128, dict(base=500000.0, scaling="yarn", factor=40.0, original_len=4096)),
+                                    (32, dict(scaling="ntk", factor=4.0)), (2, dict(scaling="linear", factor=3.0))])
+def test_rope_far_and_negative_positions(torch, sa, rot, kw, layout):
+    """Against angles from 60 decimal digits, reduced exactly: within rope_check's 2^-21 of |x1| + |x2| everywhere
+    (an angle is off by 2^-25 at most)."""
+    p = [2 ** 31 - 1, -2 ** 31, -2 ** 31 + 1, 2 ** 31 - 12345, -1, -77, 0, 5, -1000003, 2 ** 30 + 7, -2 ** 29 - 1, 2 ** 24 + 1]
+    r = sa.Rope(rot, layout=layout, **kw)
+    x = torch.randn(len(p), 3, 128, device="cuda", generator=torch.Generator(device="cuda").manual_seed(rot))
+    y, back = torch.empty_like(x), torch.empty_like(x)
+    pos = i32(torch, p)
+    mag = S.rope_frequencies(rot, **kw)[1]
+    angles = S.far_angles(p, S.rope_turns(rot, **kw))
+    for inverse, got in ((False, y), (True, back)):
+        sa.rope(r, pos, x, got, inverse=inverse)
+        for t in range(len(p)):
+            want, size = S.rope(f64(x[t:t + 1]), [1], angles[t], mag, layout, inverse)
+            tol = 2.0 ** -21 * size + 2.0 ** -24 * (np.abs(want) + 2.0 ** -21 * size)
+            assert (np.abs(f64(got[t:t + 1]) - want) <= tol).all(), p[t]

@@ -249,3 +249,34 @@ def test_a_calls_own_workspace_comes_from_the_stream_that_it_runs_on(monkeypatch
     ws = sa._call_workspace(512, t, "q", "side")
     assert (ws.n, ws.pool, current) == (512, "side", ["current"])
     assert sa._call_workspace(512, t, "q", None).pool == "current"
+
+
+# ---------------------------------------------------------------------------
+# Rotary frequencies at far positions
+# ---------------------------------------------------------------------------
+
+FREQUENCIES = [(128, {}), (256, dict(base=500000.0)), (2, dict(scaling="ntk", factor=8.0)), (96, dict(scaling="ntk", factor=4.0)),
+               (64, dict(scaling="linear", factor=3.0)), (128, dict(scaling="yarn", factor=4.0, original_len=32768)),
+               (64, dict(base=1000000.0, scaling="yarn", factor=40.0, original_len=4096))]
+
+
+@pytest.mark.parametrize("rot,kw", FREQUENCIES)
+def test_frequencies_to_a_few_units(lib, rot, kw):
+    """Against 60 decimal digits, in units u = 2^-64 turns.  Relative to w, in roundings of 2^-64 of a 64-bit
+    mantissa: the exponent |ln w|, the power 2, two pi and its division 2; a linear factor 1; ntk's base ln f r / (r - 2) + 3;
+    yarn's ramp and blend 6; and half a unit at the end."""
+    r = sa.Rope(rot, device="cpu", **kw)
+    f = kw.get("factor", 1.0)
+    for got, t in zip(r.host_freqs.numpy().view(np.uint64), S.rope_turns(rot, **kw)):
+        w = float(t) * 2 * math.pi
+        bound = 0.5 + float(t) * (abs(math.log(w)) + 14 + 2 * math.log(f))
+        assert abs(int(got) - t * 2 ** 64) <= bound < 4
+    # an angle at 2^31 positions is then off by less than 1e-8 rad; 53 bits of mantissa leave 50 units and more
+    assert 2 ** 31 * 4 * 2.0 ** -64 * 2 * math.pi < 1e-8
+
+
+def test_far_angles_are_those_of_small_positions():
+    w, _ = S.rope_frequencies(64)
+    pos = np.array([0, 1, 17, -17, 4000])
+    got, want = S.far_angles(pos, S.rope_turns(64)), pos[:, None] * w
+    assert np.abs(np.exp(1j * got) - np.exp(1j * want)).max() < 4000 * 2.0 ** -50
