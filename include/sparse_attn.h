@@ -615,8 +615,8 @@ sa_status sa_rope_frequencies(const sa_rope_scaling* desc, uint64_t* freqs, floa
  *     order of the requests (slot -1, position 0 past the last).
  * All arrays are device int32; table and free_list are updated in place, no
  * other output overlaps an input.  Where the step cannot be done (too few
- * pages, blocks or token places: SA_ERR_CAPACITY; bad lengths: SA_ERR_INVALID_ARG
- * in status, nullable) nothing changes hands: table and free_list stay, new_len
+ * pages, blocks or token places: SA_ERR_CAPACITY; bad lengths: SA_ERR_INVALID_ARG,
+ * also where both are so; in status, nullable) nothing changes hands: table and free_list stay, new_len
  * = kv_len, cu_q = 0, slots = -1, positions = 0, free_out = free_in.
  * B <= 18000, num_pages * page and max_tokens below 2^31. */
 typedef struct {

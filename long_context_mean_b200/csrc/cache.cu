@@ -253,6 +253,7 @@ sa_status launch_rows(RowArgs& a, const sa_kv4_desc& d, cudaStream_t st) {
 // is a released page, read from the ended request's row of the table; rows of
 // ended requests and entries below a request's held blocks are never written.
 constexpr int kPlanThreads = 512;
+constexpr int32_t kNone = INT32_MAX;   // no error
 
 struct PlanArgs {
   const int32_t* kv_len;
@@ -288,12 +289,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   int32_t* fresh = tok + a.B + 1;
   int32_t* gone = fresh + a.B + 1;
   __shared__ int64_t part[3][kPlanThreads / 32];
-  __shared__ int32_t bad, bad_code;
+  __shared__ int32_t bad;   // the lowest code of what is wrong, whichever thread finds it first
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) {
-    bad = 0;
-    bad_code = 0;
-  }
+  if (tid == 0) bad = kNone;
   __syncthreads();
   const int64_t count = *a.free_in;   // (with the lengths, not after them)
   const int b0 = min(a.B, tid * a.per), b1 = min(a.B, b0 + a.per);
@@ -302,13 +300,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     const int64_t old = a.kv_len[b], add = a.q_len[b];
     const int64_t most = (int64_t)a.max_blocks << a.lg_page;
     if (old < 0 || add < -1 || old > most) {
-      atomicExch(&bad, 1);
-      atomicCAS(&bad_code, 0, SA_ERR_INVALID_ARG);
+      atomicMin(&bad, SA_ERR_INVALID_ARG);
       continue;
     }
     if (add > 0 && old + add > most) {
-      atomicExch(&bad, 1);
-      atomicCAS(&bad_code, 0, SA_ERR_CAPACITY);
+      atomicMin(&bad, SA_ERR_CAPACITY);
       continue;
     }
     const int held = blocks_of(old, a.lg_page);
@@ -340,21 +336,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       total[c] += part[c][w];
     }
   if (tid == 0) {
-    int code = 0;
+    int code = kNone;
     if (count < 0 || count > a.num_pages) code = SA_ERR_INVALID_ARG;
     else if (count + total[2] > a.num_pages) code = SA_ERR_INVALID_ARG;   // more pages than there are
     else if (total[1] > count + total[2]) code = SA_ERR_CAPACITY;
     else if (total[0] > a.max_tokens) code = SA_ERR_CAPACITY;
-    if (code && !bad) {
-      bad = 1;
-      bad_code = code;
-    }
+    bad = min(bad, code);
   }
   __syncthreads();
   const int64_t gtid = (int64_t)blockIdx.x * kPlanThreads + tid, gsize = (int64_t)gridDim.x * kPlanThreads;
-  if (bad) {   // nothing is planned and nothing changes hands
+  if (bad != kNone) {   // nothing is planned and nothing changes hands
     if (gtid == 0) {
-      raise_status(a.status, bad_code);
+      raise_status(a.status, bad);
       *a.free_out = (int32_t)count;
     }
     for (int64_t b = gtid; b <= a.B; b += gsize) {

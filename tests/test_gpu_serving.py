@@ -894,3 +894,19 @@ def test_rope_far_and_negative_positions(torch, sa, rot, kw, layout):
             want, size = S.rope(f64(x[t:t + 1]), [1], angles[t], mag, layout, inverse)
             tol = 2.0 ** -21 * size + 2.0 ** -24 * (np.abs(want) + 2.0 ** -21 * size)
             assert (np.abs(f64(got[t:t + 1]) - want) <= tol).all(), p[t]
+
+
+# ---------------------------------------------------------------------------
+# The cache plan's refusals on the device
+# ---------------------------------------------------------------------------
+
+def test_cache_plan_says_the_same_of_a_step_with_two_faults(torch, sa):
+    """A request with a bad length and one without room, in either order and far apart: always the bad length."""
+    B = 600
+    for bad, full in ((0, B - 1), (B - 1, 0), (3, 4), (4, 3)):
+        new = [1] * B
+        new[bad], new[full] = -2, 1000
+        for _ in range(5):
+            k = Book(torch, sa, B, 6, B, 16, B)
+            assert k.step(new) == sa.SA_ERR_INVALID_ARG
+            assert k.new_len.tolist() == [0] * B and int(k.count_out) == B and (k.slots == -1).all()
