@@ -614,10 +614,13 @@ sa_status sa_rope_frequencies(const sa_rope_scaling* desc, uint64_t* freqs, floa
  *     [max_tokens] = each new token's place in the cache and position, in the
  *     order of the requests (slot -1, position 0 past the last).
  * All arrays are device int32; table and free_list are updated in place, no
- * other output overlaps an input.  Where the step cannot be done (too few
- * pages, blocks or token places: SA_ERR_CAPACITY; bad lengths: SA_ERR_INVALID_ARG,
- * also where both are so; in status, nullable) nothing changes hands: table and free_list stay, new_len
- * = kv_len, cu_q = 0, slots = -1, positions = 0, free_out = free_in.
+ * other output overlaps an input.  Where the step cannot be done, nothing
+ * changes hands: table and free_list stay, new_len = kv_len, cu_q = 0, slots =
+ * -1, positions = 0, free_out = free_in, and status (nullable) gets
+ * SA_ERR_INVALID_ARG for bad lengths, SA_ERR_CAPACITY for too few pages, blocks
+ * or token places, or (looked at last) SA_ERR_INVALID_ARG for a page outside
+ * the cache among those that the step releases, takes or fills up.  That a page
+ * is held or free once only is the caller's care; it is not checked.
  * B <= 18000, num_pages * page and max_tokens below 2^31. */
 typedef struct {
   int64_t B, max_blocks, num_pages, max_tokens;

@@ -345,9 +345,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   }
   __syncthreads();
   const int64_t gtid = (int64_t)blockIdx.x * kPlanThreads + tid, gsize = (int64_t)gridDim.x * kPlanThreads;
-  if (bad != kNone) {   // nothing is planned and nothing changes hands
+  auto refuse = [&](int32_t code) {   // nothing is planned and nothing changes hands
     if (gtid == 0) {
-      raise_status(a.status, bad);
+      raise_status(a.status, code);
       *a.free_out = (int32_t)count;
     }
     for (int64_t b = gtid; b <= a.B; b += gsize) {
@@ -358,14 +358,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       a.slots[t] = -1;
       a.positions[t] = 0;
     }
-    return;
-  }
+  };
+  if (bad != kNone) return refuse(bad);
+  bool wrong = false;   // a page is outside the cache
+  auto look = [&](int32_t page) { wrong |= page < 0 || page >= a.num_pages; };
+  int32_t filled = 0;   // the page of a block that is filled up, looked at after the next load or the barrier
   for (int b = b0; b < b1; ++b) {
     tok[b] = (int32_t)x[0];
     fresh[b] = (int32_t)x[1];
     gone[b] = (int32_t)x[2];
     const int64_t old = a.kv_len[b], add = a.q_len[b];
     const int held = blocks_of(old, a.lg_page);
+    look(filled);
+    if (add > 0 && (old & ((1 << a.lg_page) - 1))) filled = a.table[(int64_t)b * a.max_blocks + held - 1];
     if (add < 0) {
       x[2] += held;
     } else {
@@ -387,21 +392,31 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
   };
   auto taken = [&](int f) -> int32_t {   // the page of the f-th fresh block
     const int64_t at = top - 1 - f;
-    const int32_t page = at >= count ? released((int)(at - count)) : a.free_list[at];
-    if (page < 0 || page >= a.num_pages) {
-      raise_status(a.status, SA_ERR_INVALID_ARG);
-      return -1;
-    }
-    return page;
+    return at >= count ? released((int)(at - count)) : a.free_list[at];
   };
+  // Every page that changes hands or takes a token is looked at before anything is
+  // written: released ones, the free ones that are taken, blocks that are filled
+  // up.  Each CTA looks at all of them (no CTA writes what another looks at: entries
+  // above the old top of the stack, and blocks that no request holds yet).
+  // A thread takes a run of the released ones: one search, and loads side by side
+  // (a search for each took 2 us more).
+  for (int64_t i = top - n_fresh + tid; i < count; i += kPlanThreads) look(a.free_list[i]);
+  const int run = (n_gone + kPlanThreads - 1) / kPlanThreads;
+  for (int i = min(n_gone, tid * run), end = min(n_gone, i + run); i < end;) {
+    const int b = find(gone, a.B, i), to = min(end, gone[b + 1]);
+    const int32_t* row = a.table + (int64_t)b * a.max_blocks;
+    const int from = gone[b];
+#pragma unroll 8
+    for (; i < to; ++i) look(row[i - from]);
+  }
+  look(filled);
+  if (__syncthreads_or(wrong)) return refuse(SA_ERR_INVALID_ARG);
   // All outputs in one index space, so that their chains of loads run side by
   // side: released pages, fresh blocks, requests, tokens.
   const int64_t e1 = n_gone, e2 = e1 + n_fresh, e3 = e2 + a.B + 1, e4 = e3 + a.max_tokens;
   for (int64_t i = gtid; i < e4; i += gsize) {
     if (i < e1) {
-      const int32_t page = released((int)i);
-      if (page < 0 || page >= a.num_pages) raise_status(a.status, SA_ERR_INVALID_ARG);
-      a.free_list[count + i] = page;
+      a.free_list[count + i] = released((int)i);
     } else if (i < e2) {
       const int f = (int)(i - e1), b = find(fresh, a.B, f);
       const int held = blocks_of(a.kv_len[b], a.lg_page);
@@ -418,12 +433,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         const int old = a.kv_len[b];
         pos = old + ((int)t - tok[b]);
         const int blk = pos >> a.lg_page, held = blocks_of(old, a.lg_page);
-        int32_t page = blk < held ? a.table[(int64_t)b * a.max_blocks + blk] : taken(fresh[b] + blk - held);
-        if (page < 0 || page >= a.num_pages) {
-          raise_status(a.status, SA_ERR_INVALID_ARG);
-          page = -1;
-        }
-        if (page >= 0) slot = (page << a.lg_page) + (pos & ((1 << a.lg_page) - 1));
+        const int32_t page = blk < held ? a.table[(int64_t)b * a.max_blocks + blk] : taken(fresh[b] + blk - held);
+        slot = (page << a.lg_page) + (pos & ((1 << a.lg_page) - 1));
       }
       a.slots[t] = slot;
       a.positions[t] = pos;
@@ -481,7 +492,8 @@ sa_status launch_plan(const int32_t* kv_len, const int32_t* q_len, const sa_plan
     return set_error(SA_ERR_CUDA, "cudaFuncSetAttribute(plan_kernel) failed");
   // Every CTA repeats the scan, which costs the others nothing; how many pages are
   // released and taken is not known here, so some CTAs are there for them (256
-  // requests of up to 16,000 tokens: 4.4 us, with one CTA 9.2).
+  // requests of up to 16,000 tokens: 5.9 us, 1.6 of them the look at the pages;
+  // without it 4.3, with one CTA 9.2).
   const int64_t want = max64(8, ceil_div(max64(d.max_tokens, d.B), 2 * kPlanThreads));
   plan_kernel<<<(unsigned)min64(want, 148), kPlanThreads, smem, st>>>(a);
   return check_launch("plan_kernel");

@@ -910,3 +910,45 @@ def test_cache_plan_says_the_same_of_a_step_with_two_faults(torch, sa):
             k = Book(torch, sa, B, 6, B, 16, B)
             assert k.step(new) == sa.SA_ERR_INVALID_ARG
             assert k.new_len.tolist() == [0] * B and int(k.count_out) == B and (k.slots == -1).all()
+
+
+@pytest.mark.parametrize("where", ["free", "released", "deep in a released row", "filled up"])
+@pytest.mark.parametrize("page_id", [-1, 40, 1 << 30])
+@pytest.mark.parametrize("tokens", [200, 40000])     # 8 and 40 blocks of threads
+def test_cache_plan_with_a_page_outside_the_cache_changes_nothing(torch, sa, where, page_id, tokens):
+    k = Book(torch, sa, 5, 12, 40, 16, tokens)
+    assert k.step([33, 130, 16, 5, 0]) == 0
+    k.turn()
+    spare = k.table.clone()
+    k.table[0, 3], k.table[3, 1], k.free[30] = 1 << 20, -5, 1 << 20    # entries that the step does not come to
+    new = [1, -1, 20, 2, 3]
+    if where == "free":         # 9 pages come back, 3 are taken: the stack's own are not; so nobody ends
+        new[1] = 0
+        k.free[int(k.count) - 2] = page_id
+    elif where == "released":
+        k.table[1, 0] = page_id
+    elif where == "deep in a released row":
+        k.table[1, 7] = page_id
+    else:
+        k.table[3, 0] = page_id
+    before = [t.clone() for t in (k.table, k.free, k.kv_len, k.count)]
+    for t in (k.new_len, k.cu, k.slots, k.pos, k.count_out):
+        t.fill_(77)
+    assert k.step(new) == sa.SA_ERR_INVALID_ARG
+    for t, want in zip((k.table, k.free, k.new_len, k.count_out), before):
+        assert torch.equal(t, want)
+    assert (k.cu == 0).all() and (k.slots == -1).all() and (k.pos == 0).all()
+    # with the page put right the same step goes through, whatever stands in the entries that it does not come to
+    keep = (0, 3), (3, 1)
+    lens, free = k.kv_len.tolist(), k.free[:int(k.count)].tolist()
+    if where == "free":
+        k.free[int(k.count) - 2] = free[-2] = 40 - 1 - (int(k.count) - 2)
+    else:
+        k.table.copy_(spare)
+        for b, i in keep:
+            k.table[b, i] = before[0][b, i]
+    rows = k.table.tolist()
+    assert k.step(new) == 0
+    r = S.plan(lens, new, rows, free, 16, k.tokens)
+    assert k.table.tolist() == r["table"] and k.free[:len(r["free"])].tolist() == r["free"]
+    assert k.slots.tolist() == r["slots"] and k.new_len.tolist() == r["new_len"]
