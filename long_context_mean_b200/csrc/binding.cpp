@@ -92,6 +92,13 @@ struct Ws {
   }
 };
 
+// The C ABI's scale has 32 bits, and 0 there means 1 / sqrt(d).
+float scale32(double scale) {
+  const float s = (float)scale;
+  need(s != 0.f || scale == 0.0, "scale must be 0 or a number that 32 bits hold");
+  return s;
+}
+
 // call(stream) with `dev` current, on the given stream or the device's current one.
 template <class F>
 int on(c10::Device dev, std::optional<uintptr_t> stream, F call) {
@@ -105,6 +112,7 @@ using Stream = std::optional<uintptr_t>;
 int window_attn(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& out, const Maybe& lse, int64_t window,
                 int64_t sinks, const Maybe& q_len, const Maybe& kv_len, double scale, const Maybe& status,
                 const Tensor& ws, int32_t flags, Stream stream) {
+  const float sc = scale32(scale);
   need(q.dim() == 4 && k.dim() == 4, "q and k must have four axes");
   const auto dev = q.device();
   const auto dt = q.scalar_type();
@@ -118,7 +126,7 @@ int window_attn(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor&
   int32_t* st = index(status, 1, "status", dev);
   const Ws w(ws, dev);
   return on(dev, stream, [&](void* cs) {
-    return entry.window_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), &s, window, sinks, ql, kl, (float)scale,
+    return entry.window_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), &s, window, sinks, ql, kl, sc,
                              out.data_ptr(), lse ? static_cast<float*>(lse->data_ptr()) : nullptr, st, w.ptr, w.bytes,
                              flags, cs);
   });
@@ -162,6 +170,7 @@ int kv4_read(const Tensor& pages, int64_t page, int64_t d, const Tensor& slots, 
 int kv4_attn(const Tensor& q, const Tensor& pages, int64_t page, int64_t d, const Tensor& table, const Tensor& kv_len,
              const Tensor& out, const Maybe& lse, const Tensor& cu_q, int64_t window, int64_t sinks, double scale,
              const Maybe& status, const Tensor& ws, Stream stream) {
+  const float sc = scale32(scale);
   const auto dev = pages.device();
   const sa_kv4_desc desc = describe(pages, page, d);
   need(q.dim() == 3 && table.dim() == 2, "q must have three axes and table two");
@@ -175,7 +184,7 @@ int kv4_attn(const Tensor& q, const Tensor& pages, int64_t page, int64_t d, cons
   const Ws w(ws, dev);
   return on(dev, stream, [&](void* cs) {
     return entry.kv4_attn(q.data_ptr(), T, Hq, qs.strides, cu, B, pages.data_ptr(), &desc,
-                          static_cast<const int32_t*>(table.data_ptr()), blocks, kl, window, sinks, (float)scale,
+                          static_cast<const int32_t*>(table.data_ptr()), blocks, kl, window, sinks, sc,
                           out.data_ptr(), lse ? static_cast<float*>(lse->data_ptr()) : nullptr, st, w.ptr, w.bytes, cs);
   });
 }

@@ -280,3 +280,24 @@ def test_far_angles_are_those_of_small_positions():
     pos = np.array([0, 1, 17, -17, 4000])
     got, want = S.far_angles(pos, S.rope_turns(64)), pos[:, None] * w
     assert np.abs(np.exp(1j * got) - np.exp(1j * want)).max() < 4000 * 2.0 ** -50
+
+
+# ---------------------------------------------------------------------------
+# A scale below 32 bits' range
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("scale", [1e-50, -1e-50, 5e-324])
+def test_a_scale_that_32_bits_round_to_zero_is_not_the_default(lib, scale):
+    """0 means 1 / sqrt(d); a scale that is not 0 never does."""
+    import torch
+    q = torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="scale"):
+        sa.window_attn(q, q, q, torch.zeros_like(q), scale=scale, ws=ws)
+    cache = sa.KV4Cache.allocate(2, 2, 16, 64, device="cpu")
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="scale"):
+        sa.kv4_attn(q[0], cache, i[None], i[:1], torch.zeros_like(q[0]), cu_q=i, scale=scale, ws=ws)
+    for good in (0.0, -0.0, 2e-45, 0.5):      # these come as far as the tensors' device
+        with pytest.raises(ValueError, match="CUDA device"):
+            sa.window_attn(q, q, q, torch.zeros_like(q), scale=good, ws=ws)
