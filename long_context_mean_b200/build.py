@@ -5,7 +5,8 @@ an object (in parallel, only when a source or header is newer than its
 object) and links them into ``long_context_mean_b200/libsparseattn.so``.
 The CUDA runtime is linked statically; no libcuda link is needed (driver
 entry points are fetched at run time).  ``csrc/binding.cpp`` becomes
-``_serve.so``, the compiled Python binding of the serving operators.
+``_serve.so``, the compiled Python binding of the serving operators; it alone
+needs torch, the Python headers and g++, and without them only it is left out.
 """
 
 from __future__ import annotations
@@ -16,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -57,6 +59,10 @@ def _compile(src: str, extra: list[str], verbose: bool) -> str:
     return obj
 
 
+class BindingUnavailable(RuntimeError):
+    """What the Python binding is built with is not there (the C library needs none of it)."""
+
+
 def build_binding(verbose: bool = False) -> str:
     """The compiled Python binding of the serving operators (csrc/binding.cpp, host code against torch's headers)."""
     src = os.path.join(CSRC, "binding.cpp")
@@ -64,10 +70,18 @@ def build_binding(verbose: bool = False) -> str:
         return BINDING
     import sysconfig
 
-    import torch
-    from torch.utils import cpp_extension
+    try:
+        import torch
+        from torch.utils import cpp_extension
+    except ImportError as e:
+        raise BindingUnavailable(f"torch cannot be imported: {e}") from e
+    if shutil.which("g++") is None:
+        raise BindingUnavailable("g++ not found")
     inc = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"], INCLUDE,
            os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    for header in ("Python.h", "torch/csrc/utils/pybind.h", "cuda_runtime_api.h"):
+        if not any(os.path.exists(os.path.join(d, header)) for d in inc):
+            raise BindingUnavailable(f"the header {header} was not found")
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            "-DTORCH_EXTENSION_NAME=_serve", *[x for d in inc for x in ("-isystem", d)], src, "-o", BINDING + ".tmp",
@@ -95,13 +109,16 @@ def build(verbose: bool = False, extra: list[str] | None = None, force: bool = F
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
         binding = ex.submit(build_binding, verbose)
         objs = list(ex.map(lambda s: _compile(s, extra, verbose), srcs))
-        binding.result()
     if not os.path.exists(LIB) or os.path.getmtime(LIB) < max(os.path.getmtime(o) for o in objs):
         cmd = [nvcc(), *ARCH, "-shared", "-o", LIB + ".tmp", *objs]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(LIB + ".tmp", LIB)
+    try:
+        binding.result()
+    except BindingUnavailable as e:
+        warnings.warn(f"libsparseattn.so is built, its Python binding of the serving operators is not: {e}", stacklevel=2)
     return LIB
 
 
