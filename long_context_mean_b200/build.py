@@ -59,6 +59,16 @@ def _compile(src: str, extra: list[str], verbose: bool) -> str:
     return obj
 
 
+def _binding_world() -> str:
+    """The interpreter and the torch that a binding is built for, and works with."""
+    import importlib.metadata
+    try:
+        torch = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        torch = "none"
+    return f"{sys.implementation.cache_tag} torch {torch}"
+
+
 class BindingUnavailable(RuntimeError):
     """What the Python binding is built with is not there (the C library needs none of it)."""
 
@@ -66,8 +76,10 @@ class BindingUnavailable(RuntimeError):
 def build_binding(verbose: bool = False) -> str:
     """The compiled Python binding of the serving operators (csrc/binding.cpp, host code against torch's headers)."""
     src = os.path.join(CSRC, "binding.cpp")
+    stamp, world = os.path.join(BUILD, "_serve.stamp"), _binding_world()
     if os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(os.path.getmtime(src), _newest_header()):
-        return BINDING
+        if os.path.exists(stamp) and open(stamp).read() == world:
+            return BINDING
     import sysconfig
 
     try:
@@ -84,7 +96,7 @@ def build_binding(verbose: bool = False) -> str:
             raise BindingUnavailable(f"the header {header} was not found")
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
-           "-DTORCH_EXTENSION_NAME=_serve", *[x for d in inc for x in ("-isystem", d)], src, "-o", BINDING + ".tmp",
+           "-DTORCH_EXTENSION_NAME=_serve", f'-DBUILT_FOR_TORCH="{torch.__version__}"', *[x for d in inc for x in ("-isystem", d)], src, "-o", BINDING + ".tmp",
            "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"]
     if verbose:
         print(" ".join(cmd), flush=True)
@@ -92,6 +104,8 @@ def build_binding(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
     os.replace(BINDING + ".tmp", BINDING)
+    with open(stamp, "w") as f:
+        f.write(world)
     return BINDING
 
 

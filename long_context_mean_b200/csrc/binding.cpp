@@ -261,6 +261,7 @@ int cache_plan(const Tensor& kv_len, const Tensor& q_len, const Tensor& table, c
 }  // namespace
 
 PYBIND11_MODULE(_serve, m) {
+  m.attr("built_for_torch") = BUILT_FOR_TORCH;
   m.def("bind", &bind);
   m.def("window_attn", &window_attn);
   m.def("kv4_append", &kv4_append);

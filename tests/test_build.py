@@ -40,3 +40,34 @@ def test_a_binding_that_does_not_compile_is_an_error_behind_the_library(fresh, m
     with pytest.raises(RuntimeError, match="binding.cpp"):
         B.build()
     assert os.path.exists(B.LIB)
+
+
+def test_the_binding_is_built_again_for_another_torch(tmp_path, monkeypatch):
+    import importlib.metadata
+    from types import SimpleNamespace
+    monkeypatch.setattr(B, "BINDING", str(tmp_path / "_serve.so"))
+    monkeypatch.setattr(B, "BUILD", str(tmp_path))
+    runs = []
+
+    def compiled(cmd, **kw):
+        runs.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return SimpleNamespace(returncode=0)
+    monkeypatch.setattr(B.subprocess, "run", compiled)
+    for version, n in (("1.0", 1), ("1.0", 1), ("1.1", 2), ("1.1", 2)):
+        monkeypatch.setattr(importlib.metadata, "version", lambda name, v=version: v)
+        B.build_binding()
+        assert len(runs) == n
+
+
+def test_a_binding_for_another_torch_is_refused(monkeypatch):
+    import torch
+
+    from long_context_mean_b200 import sa
+    B.build()
+    monkeypatch.setattr(sa, "_serve", None)
+    sa._binding()
+    monkeypatch.setattr(sa, "_serve", None)
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    with pytest.raises(RuntimeError, match="built for torch"):
+        sa._binding()
