@@ -952,3 +952,129 @@ def test_cache_plan_with_a_page_outside_the_cache_changes_nothing(torch, sa, whe
     r = S.plan(lens, new, rows, free, 16, k.tokens)
     assert k.table.tolist() == r["table"] and k.free[:len(r["free"])].tolist() == r["free"]
     assert k.slots.tolist() == r["slots"] and k.new_len.tolist() == r["new_len"]
+
+
+# ---------------------------------------------------------------------------
+# The kernels' forms for large calls
+# ---------------------------------------------------------------------------
+
+LARGE_SIMT = [     # 592 tiles of 16 rows and more: two warps a tile
+    (2, 8, 4, 600, 640, 64, "fp32", 100, 3, [600, 417], [640, 417]),
+    (1, 16, 4, 595, 595, 128, "fp32", 0, 0, None, None),
+    (3, 8, 8, 400, 400, 16, "fp32", 33, 9, [400, 1, 0], [390, 400, 77]),
+    (1, 16, 2, 600, 633, 256, "fp32", 64, 1, None, None),
+    (2, 8, 2, 600, 600, 96, "bf16", 70, 2, [600, 599], [600, 600]),
+]
+
+
+@pytest.mark.parametrize("c", LARGE_SIMT, ids=lambda c: "-".join(map(str, c[:9])))
+@pytest.mark.parametrize("poison", [False, True])
+def test_window_attn_many_rows_on_the_cuda_cores(torch, sa, c, poison):
+    test_window_attn(torch, sa, c, 0, poison)
+
+
+@pytest.mark.parametrize("c", [(1, 4, 1, 1, 20000, 128, "bf16", 0, 0, None, None),
+                               (4, 8, 2, 1, 3001, 128, "bf16", 0, 0, None, [3001, 1, 2999, 0]),
+                               (1, 8, 1, 4, 9000, 64, "bf16", 0, 0, None, None),
+                               (1, 16, 1, 3, 12000, 128, "bf16", 9000, 500, None, None)],
+                         ids=lambda c: "-".join(map(str, c[:9])))
+def test_window_attn_few_rows_over_many_keys(torch, sa, c):
+    """Units of more parts than one round of the join takes."""
+    test_window_attn(torch, sa, c, 8, False)
+
+
+@pytest.mark.parametrize("c", [(4, 1, 128, 64, [20000], [1], 0, 0), (4, 1, 64, 16, [20011], [1], 0, 0),
+                               (4, 1, 128, 64, [20000], [4], 0, 0), (8, 2, 64, 128, [21003], [2], 15000, 300),
+                               (8, 2, 128, 64, [1, 30000, 1, 2], [1, 1, 1, 1], 0, 0),
+                               (8, 2, 64, 32, [30000, 3, 1, 900], [1, 3, 1, 5], 0, 0)],
+                         ids=lambda c: "-".join(map(str, c)).replace(" ", ""))
+def test_kv4_attn_many_keys(torch, sa, c):
+    test_kv4_attn(torch, sa, c)
+
+
+@pytest.mark.parametrize("H,d,T", [(8, 128, 700), (8, 128, 1001), (8, 128, 2000), (5, 128, 2000), (5, 64, 2000), (8, 64, 1999)])
+def test_kv4_rows_of_a_prompt(torch, sa, H, d, T):
+    """Warps that walk 2, 3 and 4 blocks of heads, with and without a tail; runs of tokens, single ones and left out ones."""
+    g = torch.Generator(device="cuda").manual_seed(T + H)
+    page = 32
+    pages = T // page + 5
+    k, v = (torch.randn(T, H, d, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    k[3, H - 1, :32], v[T - 1, H - 1, 5] = 0, math.nan
+    slots = torch.arange(T, device="cuda", dtype=torch.int32) + 5        # a run from an odd place
+    some = torch.randperm(T, device="cuda", generator=g)[:T // 3]
+    slots[some] = slots[some[torch.randperm(len(some), device="cuda", generator=g)]]
+    slots[some[:4]] = -1
+    cache = sa.KV4Cache.allocate(pages, H, page, d)
+    cache.pages.fill_(0x5A)
+    status = i32(torch, [0])
+    sa.kv4_append(k, v, slots, cache, status=status)
+    want = np.full(cache.pages.shape, 0x5A, np.uint8)
+    sl = slots.cpu().numpy()
+    (kc, ks), (vc, vs) = S.quantise(f64(k)), S.quantise(f64(v))
+    for t in range(T):
+        for h in range(H):
+            if sl[t] >= 0:
+                S.store(want, sl[t], h, kc[t, h], ks[t, h], vc[t, h], vs[t, h])
+    assert np.array_equal(cache.pages.cpu().numpy(), want)
+    ko, vo = (torch.full((T, H, d), 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    sa.kv4_read(cache, slots, ko, vo, status=status)
+    assert sa.read_status(status) == 0
+    for got, c, s in ((ko, kc, ks), (vo, vc, vs)):
+        x = S.values(c, s)
+        x = S.round_bf16(np.nan_to_num(x, nan=0)) + np.where(np.isnan(x), np.nan, 0)
+        x[sl < 0] = 9
+        assert np.array_equal(f64(got), x, equal_nan=True)
+
+
+@pytest.mark.parametrize("B,page,max_new", [(5000, 16, 5), (18000, 32, 2)])
+def test_cache_plan_of_many_requests(torch, sa, B, page, max_new):
+    test_cache_plan_steps(torch, sa, B, page, max_new)
+
+
+@pytest.mark.parametrize("c", [(2400, 2, 1, 66, 6, "interleaved", "bf16", {}), (2401, 3, 2, 35, 2, "half", "fp32", {}),
+                               (2403, 1, 1, 72, 72, "half", "bf16", {})], ids=lambda c: "-".join(map(str, c[:7])))
+@pytest.mark.parametrize("inverse", [False, True])
+def test_rope_of_many_tokens_without_aligned_vectors(torch, sa, c, inverse):
+    test_rope(torch, sa, c, inverse)
+
+
+@pytest.mark.parametrize("op", ["window", "kv4"])
+def test_a_captured_call_on_a_forked_stream_has_a_workspace_of_its_own(torch, sa, op):
+    """In a captured graph, calls without `ws` run on a forked stream beside work of the capturing one, which
+    allocates and frees blocks of the workspace's size in between; every replay gives what the calls give."""
+    if op == "kv4":
+        q, cache, table, kv_len, cu, _ = paged(torch, sa, (32, 8, 128, 64, [3000], [1], 0, 0))
+        q, table = q[:1], table.cuda()
+        n = sa.kv4_attn_workspace(cache, 32)
+
+        def call(out, **kw):
+            sa.kv4_attn(q, cache, table, kv_len, out, cu_q=cu, **kw)
+    else:
+        q, k, v, _, _ = window_inputs(torch, (2, 32, 8, 1, 3000, 128, "bf16", 0, 0, None, None))
+        n = sa.window_attn_workspace(q, k, v)
+
+        def call(out, **kw):
+            sa.window_attn(q, k, v, out, flags=8, **kw)
+    want, outs = torch.empty_like(q), [torch.empty_like(q) for _ in range(4)]
+    call(want)
+    kept = torch.empty(4, n, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        for i, out in enumerate(outs):
+            call(out, stream=side)
+            temp = torch.full((n,), i, dtype=torch.uint8, device="cuda")
+            temp += 10
+            kept[i].copy_(temp)
+            del temp
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(10):
+        kept.zero_()
+        for out in outs:
+            out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, want) for out in outs)
+        assert all((kept[i] == 10 + i).all() for i in range(4))
