@@ -489,7 +489,9 @@ typedef struct {
  * were.  bf16 with d in {64, 128} runs on the tensor cores; fp32, and other
  * d up to 256 with d * elem_size a multiple of 16, on the CUDA cores.  All
  * tensors 16-byte aligned; lse is nullable; out overlaps no input; Nq * Hq
- * below 2^31.  ws:
+ * below 2^31.  On the tensor cores the softmax's weights are rounded to bf16
+ * before they multiply V, as in sa_block_sparse_attn (their sum is not: lse
+ * has 32 bits); on the CUDA cores they stay fp32.  ws:
  * sa_window_attn_workspace() bytes (0 for an invalid shape), 256-byte aligned;
  * calls that share it must not overlap on the GPU, captured ones included.
  * flags: 0, or one of SA_FLAG_FORCE_SIMT, SA_FLAG_FORCE_DECODE,
@@ -542,7 +544,8 @@ sa_status sa_kv4_read(const void* cache, const sa_kv4_desc* desc, const int32_t*
  * may hold anything.  kv_len: device int32 [B], the new tokens included.
  * window and sinks as above.  Few new tokens a sequence are what it is made
  * for: every 16 rows (tokens times query heads of a kv head) read the cache
- * once.  Queries above 2^100 in magnitude, and values of V above 2^50, overflow;
+ * once.  The softmax's weights, and then their products with V's scales, are
+ * rounded to bf16 (the weights' sum is not).  Queries above 2^100 in magnitude, and values of V above 2^50, overflow;
  * weights times scales of V below 2^-57 are lost.  T * Hq below 2^31.  Should
  * a wait for a copy run out (2 s; status SA_ERR_TIMEOUT), its block stops:
  * the rows that it works on stay as they were or become NaN.  ws:

@@ -31,6 +31,9 @@
 //    shift, AND-OR and subtraction took 108, 8-bit operands (converted back to
 //    fp16 by the compiler) 165.  Contiguous bf16, 48 single tokens over up to 4352
 //    keys of 8 heads, 513 MB: 84 us (6.1 TB/s).
+//  * times here are the GPU's alone, over the same inputs again; through the call, on
+//    inputs that change, those 48 tokens take 88 us, and 16 sequences of 4 to 131,072
+//    tokens 105 where they take 97.
 // Rounding: P (and P times the V scale) is rounded to bf16 for the second
 // product; sums, maxima and outputs are fp32.
 #include <cuda_fp16.h>
@@ -238,7 +241,7 @@ struct Kv4 {
   // What a unit costs beside its tiles, in tiles (its lengths, queries and output
   // are a chain of memory latencies): without it a piece of many one-token
   // sequences takes longest, and the batch nearly twice the time: 16 sequences of 4
-  // to 131,072 tokens take 98 us with 8.
+  // to 131,072 tokens take 97 us with 8.
   static constexpr int COST = 8;
   // Channel of accumulator tile j's row lane / 4 (+ 8 where half).
   static __device__ __forceinline__ int channel(int j, int half, int r) { return 32 * (j >> 1) + 4 * r + 2 * (j & 1) + half; }

@@ -15,7 +15,7 @@
 // computes their cos and sin once into shared memory (one pair per thread) and
 // all heads of q and k use them, so the trigonometry is 1 / (Hq + Hk) of the
 // pairs and one launch serves both tensors.  16,411 tokens, 32 + 8 heads of 128 in
-// bf16: 60 us, 5.6 TB/s.
+// bf16: 59.5 us on the GPU, 5.6 TB/s; through the call, on inputs that change, 63.
 #include <cmath>
 
 #include "sa_internal.cuh"

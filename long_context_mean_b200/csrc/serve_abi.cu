@@ -45,7 +45,8 @@ bool on_tensor_cores(const sa_window_shape& s) { return s.dtype == SA_BF16 && (s
 // 4096 keys 128 tokens 69 and 70, 256 tokens 128 and 71; over 512 keys 32 tokens 12.6
 // and 14.5, 64 tokens 14.8 and 14.6, 128 tokens 19.6 and 14.7.  Heads of 64, 4096
 // keys: 128 tokens 46 and 58, 192 tokens 66 and 60.  24 heads of 128 of their own, 4
-// sequences of 4096 keys: 32 tokens 56 and 58, 64 tokens 100 and 58.
+// sequences of 4096 keys: 32 tokens 56 and 58, 64 tokens 100 and 58.  (A causal
+// prompt over itself is charged all of its keys, of which its units see half.)
 bool prefill_wins(const sa_window_shape& s, int64_t window, int64_t sinks) {
   const int64_t group = s.Hq / s.Hkv, tiles = ceil_div(s.Nq, 128);
   const int64_t units = s.B * (group % 2 == 0 ? s.Hq / 2 * tiles : s.Hq * ceil_div(tiles, 2));

@@ -16,7 +16,7 @@
 // keys interleaved so that a warp's 4 row groups and 8 key groups each read one
 // wavefront of shared memory: 8 wavefronts feed 64 multiply-adds a lane.  K and then
 // V of a tile go through one buffer a warp; 16 warps an SM (d = 64) cover its
-// latency.  2 x 1000 rows, 8 heads, d = 64, window 256: 55 us (64 x 64 tiles of a
+// latency.  2 x 1000 rows, 8 heads, d = 64, window 256: 57 us (64 x 64 tiles of a
 // block, and 32 x 32 tiles with 8 rows a lane and two buffers, 80: 8 warps an SM
 // leave the pipes idle half the time).
 #include "sa_internal.cuh"

@@ -26,8 +26,8 @@
 //  * O is rescaled only when a row's maximum grows by more than 2^8.
 // 16,384 rows, 32/8 heads of 128, window 4096, 128 sinks: 855 us, 1155 TFLOP/s of
 // visible pairs, some 3100 clocks for two tiles of 2048 clocks of mma; three padded
-// prompts of up to 2777 rows, window 1024: 102 us, where a unit of ten tiles pays
-// its start and its output.
+// prompts of up to 2777 rows, window 1024: 99 us over the same inputs again, 111 on inputs
+// that change; a unit of ten tiles there pays its start and its output.
 // Roundings: P is rounded to bf16 for the second product (l sums the unrounded
 // values); everything else is fp32.
 // V rows that no row of the unit sees (behind a sequence of a padded batch,
@@ -370,7 +370,7 @@ __device__ void softmax_rows(const Params& p, Ctl* c, uint8_t* smem, uint32_t tm
         const int key = k0 + row;
         if (key >= u.hi || (key < u.lo && key >= u.n_sink)) {
           // the swizzle moves 16-byte pieces within a row's 128 bytes: the whole row is
-          // zeroed, neighbouring lanes in other banks (in one, 108 us where this takes 102)
+          // zeroed, neighbouring lanes in other banks (in one, the padded prompts take 6% longer)
           uint4* v = reinterpret_cast<uint4*>(smem + C::OFF_KV + (itv % kStages) * C::TILE_BYTES + row * 128);
 #pragma unroll
           for (int x = 0; x < C::CHUNKS; ++x)

@@ -501,8 +501,10 @@ def window_attn(q, k, v, out, lse=None, *, window=0, sinks=0, q_len=None, kv_len
     and the first `sinks` ones: q, out [B, Hq, Nq, d], k, v [B, Hkv, Nk, d], lse
     [B, Hq, Nq] float32.  Row i of a sequence with n_q rows and n_k keys
     sits at position n_k - n_q + i; q_len, kv_len (int32 [B]) are the lengths
-    of a padded batch, and rows past q_len stay as they were.  ws: a
-    workspace() of window_attn_workspace() bytes (allocated per call if None)."""
+    of a padded batch, and rows past q_len stay as they were.  bf16 with d 64
+    or 128 rounds the softmax's weights to bf16 before they multiply v; fp32 and
+    other d do not.  ws: a workspace() of window_attn_workspace() bytes
+    (allocated per call, on the call's stream, if None)."""
     if ws is None:
         ws = _call_workspace(window_attn_workspace(q, k, v), q, "q", stream)
     code = _binding().window_attn(q, k, v, out, lse, window, sinks, q_len, kv_len, scale, status, ws, flags, _raw(stream))
@@ -556,7 +558,9 @@ def kv4_attn(q, cache: KV4Cache, table, kv_len, out, lse=None, *, cu_q, window=0
     """Attention of the tokens q (bf16 [T, Hq, d]) over the cache.  Sequence b
     has the tokens cu_q[b] : cu_q[b + 1] (int32 [B + 1]), the last of its
     kv_len[b] (int32 [B]) keys, in the pages table[b] (int32 [B, max_blocks]).
-    out bf16 [T, Hq, d], lse float32 [T, Hq]; window and sinks as in window_attn."""
+    out bf16 [T, Hq, d], lse float32 [T, Hq]; window, sinks and ws as in
+    window_attn.  The softmax's weights and their products with v's scales are
+    rounded to bf16."""
     if ws is None:
         ws = _call_workspace(kv4_attn_workspace(cache, q.shape[1]), cache.pages, "the cache", stream)
     code = _binding().kv4_attn(q, cache.pages, cache.page, cache.d, table, kv_len, out, lse, cu_q, window, sinks, scale,
@@ -608,7 +612,8 @@ def cache_plan(kv_len, q_len, table, free_list, free_count, page, new_len, cu_q,
     table [B, max_blocks] and the stack free_list [num_pages] (free_count [1]
     of them free) in place; writes new_len [B], cu_q [B + 1], slots and
     positions [max_tokens] and free_count_out [1].  If there are too few pages
-    (status SA_ERR_CAPACITY) nothing changes hands."""
+    (status SA_ERR_CAPACITY), or a length or a page is outside its range
+    (SA_ERR_INVALID_ARG), nothing changes hands."""
     code = _binding().cache_plan(kv_len, q_len, table, free_list, free_count, page, new_len, cu_q, slots, positions,
                                  free_count_out, status, _raw(stream))
     if code != SA_OK:
