@@ -453,9 +453,10 @@ def _binding():
             raise RuntimeError("_serve.so cannot be loaded: build it with `python -m long_context_mean_b200.build` "
                                f"(there is no fallback implementation): {e}") from e
         import torch
-        if m.built_for_torch != torch.__version__:
-            raise RuntimeError(f"_serve.so was built for torch {m.built_for_torch}, this is {torch.__version__}: build it "
-                               "again with `python -m long_context_mean_b200.build`")
+        built_for = getattr(m, "built_for_torch", "of an unknown version")
+        if built_for != torch.__version__:
+            raise RuntimeError(f"_serve.so was built for torch {built_for}, this is {torch.__version__}: build it again with "
+                               "`python -m long_context_mean_b200.build`")
         m.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in SERVE_ENTRIES})
         _serve = m
     return _serve

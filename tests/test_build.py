@@ -71,3 +71,16 @@ def test_a_binding_for_another_torch_is_refused(monkeypatch):
     monkeypatch.setattr(torch, "__version__", "0.0.1")
     with pytest.raises(RuntimeError, match="built for torch"):
         sa._binding()
+
+
+def test_a_binding_that_does_not_say_its_torch_is_refused(monkeypatch):
+    """One built before the version was kept in it."""
+    from types import SimpleNamespace
+
+    import long_context_mean_b200 as package
+    from long_context_mean_b200 import sa
+    B.build()
+    monkeypatch.setattr(sa, "_serve", None)
+    monkeypatch.setattr(package, "_serve", SimpleNamespace(bind=lambda at: None), raising=False)
+    with pytest.raises(RuntimeError, match="unknown version"):
+        sa._binding()
